@@ -26,7 +26,9 @@ lib = None
 Q4_0 = 2
 Q8_0 = 8
 Q4_K = 12
-TYPES = {"q4_0": Q4_0, "q8_0": Q8_0, "q4_k": Q4_K, Q4_0: Q4_0, Q8_0: Q8_0, Q4_K: Q4_K}
+MXFP4 = 39
+TYPES = {"q4_0": Q4_0, "q8_0": Q8_0, "q4_k": Q4_K, "mxfp4": MXFP4, Q4_0: Q4_0, Q8_0: Q8_0,
+         Q4_K: Q4_K, MXFP4: MXFP4}
 MAX_BATCH = 256
 
 STATUS = {0: "GQ_OK", -1: "GQ_ERR_NULL", -2: "GQ_ERR_SHAPE", -3: "GQ_ERR_TYPE",
@@ -39,6 +41,9 @@ EXPORTS = ("gq_abi_version", "gq_block_bytes", "gq_row_bytes", "gq_quantize_q4_0
            "gq_mul_mat_ws", "gq_mul_mat_noalloc", "gq_mul_mat_batched",
            "gq_mul_mat_batched_workspace_size", "gq_mul_mat_batched_ws", "gq_mul_mat_q8x",
            "gq_mul_mat_q8x_batched", "gq_mul_mat_rmsnorm", "gq_mul_mat_swiglu",
+           "gq_quantize_mxfp4", "gq_mul_mat_mx4x", "gq_mul_mat_mx4x_ws",
+           "gq_mul_mat_mx4x_workspace_size", "gq_moe_route", "gq_moe_swiglu",
+           "gq_moe_swiglu_ws", "gq_moe_workspace_size",
            "gq_get_last_error",
            "gq_selftest_wait_timeout", "gq_status_string",
            # include/gq_gguf.h
@@ -53,6 +58,13 @@ class Problem(ctypes.Structure):
     """gq_mul_mat_problem."""
     _fields_ = [("W_blocks", ctypes.c_void_p), ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p),
                 ("M", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class Experts(ctypes.Structure):
+    """gq_moe_experts."""
+    _fields_ = [("W_gate", ctypes.c_void_p), ("W_up", ctypes.c_void_p), ("W_down", ctypes.c_void_p),
+                ("type", ctypes.c_int), ("down_type", ctypes.c_int), ("E", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("F", ctypes.c_int64)]
 
 
 class GgufTensor(ctypes.Structure):
@@ -71,7 +83,7 @@ def load(path: str = LIB_PATH):
     L.gq_abi_version.argtypes, L.gq_abi_version.restype = [], i32
     L.gq_block_bytes.argtypes, L.gq_block_bytes.restype = [ctypes.c_int], ctypes.c_size_t
     L.gq_row_bytes.argtypes, L.gq_row_bytes.restype = [ctypes.c_int, i64], ctypes.c_size_t
-    for q in (L.gq_quantize_q4_0, L.gq_quantize_q8_0, L.gq_quantize_q4_k):
+    for q in (L.gq_quantize_q4_0, L.gq_quantize_q8_0, L.gq_quantize_q4_k, L.gq_quantize_mxfp4):
         q.argtypes, q.restype = [vp, i64, i64, vp, vp], ctypes.c_int
     L.gq_dequantize.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp]
     L.gq_dequantize.restype = ctypes.c_int
@@ -99,6 +111,18 @@ def load(path: str = LIB_PATH):
     L.gq_mul_mat_swiglu.restype = ctypes.c_int
     L.gq_mul_mat_q8x_batched.argtypes = [ctypes.POINTER(Problem), i32, ctypes.c_int, i64, vp]
     L.gq_mul_mat_q8x_batched.restype = ctypes.c_int
+    sz, xp = ctypes.c_size_t, ctypes.POINTER(Experts)
+    L.gq_mul_mat_mx4x.argtypes = [vp, ctypes.c_int, i64, i64, vp, i64, vp, vp]
+    L.gq_mul_mat_mx4x_ws.argtypes = [vp, ctypes.c_int, i64, i64, vp, i64, vp, vp, sz, vp]
+    L.gq_mul_mat_mx4x_workspace_size.argtypes = [ctypes.c_int, i64, i64, i64]
+    L.gq_moe_route.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
+    L.gq_moe_swiglu.argtypes = [xp, vp, i64, vp, vp, i32, vp, vp]
+    L.gq_moe_swiglu_ws.argtypes = [xp, vp, i64, vp, vp, i32, vp, vp, sz, vp]
+    L.gq_moe_workspace_size.argtypes = [xp, i64, i32]
+    for fn in (L.gq_mul_mat_mx4x, L.gq_mul_mat_mx4x_ws, L.gq_moe_route, L.gq_moe_swiglu,
+               L.gq_moe_swiglu_ws):
+        fn.restype = ctypes.c_int
+    L.gq_mul_mat_mx4x_workspace_size.restype = L.gq_moe_workspace_size.restype = sz
     L.gq_get_last_error.argtypes, L.gq_get_last_error.restype = [vp], ctypes.c_int
     L.gq_selftest_wait_timeout.argtypes = [i64, vp]
     L.gq_selftest_wait_timeout.restype = ctypes.c_int
@@ -203,7 +227,7 @@ def quantize(W: torch.Tensor, t, out: torch.Tensor | None = None, stream=None) -
     if out is None:
         out = torch.empty((M, row_bytes(t, K)), dtype=torch.uint8, device=W.device)
     fn = {Q4_0: lib.gq_quantize_q4_0, Q8_0: lib.gq_quantize_q8_0,
-          Q4_K: lib.gq_quantize_q4_k}[_type(t)]
+          Q4_K: lib.gq_quantize_q4_k, MXFP4: lib.gq_quantize_mxfp4}[_type(t)]
     _check(fn(_dev(W, torch.float32, "W"), M, K, _dev(out, torch.uint8, "W_blocks"),
               _stream(stream)), "gq_quantize")
     return out
@@ -373,6 +397,121 @@ def mul_mat_q8x_batched(problems, t, N: int, stream=None) -> None:
         problems = make_problems(problems)
     _check(lib.gq_mul_mat_q8x_batched(problems, problems._count, _type(t), N, _stream(stream)),
            "gq_mul_mat_q8x_batched")
+
+
+def _call_stream(stream, *tensors) -> int:
+    """The stream of a call on these tensors: CUDA ones must live on the current device, where
+    the library launches."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream` (None: torch's current one)."""
+    out = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:   # else its memory could be handed on before the call has written it
+        out.record_stream(stream)
+    return out
+
+
+def _tokens(X: torch.Tensor, K: int, name: str = "X") -> torch.Tensor:
+    if X.dim() == 1:
+        X = X.view(1, -1)
+    if X.dim() != 2 or X.shape[1] != K:
+        raise ValueError(f"{name} must be (N, {K})")
+    return X
+
+
+def _has(t: torch.Tensor, n: int, name: str) -> None:
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
+
+
+def mul_mat_mx4x(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Y (N, M) with X quantized to MXFP4 like the weights (t must be mxfp4). With a
+    `workspace` (uint8 CUDA tensor of mx4x_workspace_size bytes) the call can be captured."""
+    X = _tokens(X, K)
+    N = X.shape[0]
+    _has(blocks, M * row_bytes(t, K), "W_blocks")
+    if out is None:
+        out = _new((N, M), torch.float32, X.device, stream) if X.is_cuda else _out_like(X, (N, M))
+    _has(out, N * M, "Y")
+    args = (_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K, _act(X, torch.float32, "X"), N,
+            _act(out, torch.float32, "Y"))
+    s = _call_stream(stream, blocks, X, out)
+    if workspace is None:
+        _check(lib.gq_mul_mat_mx4x(*args, s), "gq_mul_mat_mx4x")
+    else:
+        _check(lib.gq_mul_mat_mx4x_ws(*args, _dev(workspace, torch.uint8, "workspace"),
+                                      workspace.numel(), s), "gq_mul_mat_mx4x_ws")
+    return out
+
+
+def mx4x_workspace_size(t, M: int, K: int, N: int) -> int:
+    return int(lib.gq_mul_mat_mx4x_workspace_size(_type(t), M, K, N))
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, stream=None):
+    """(ids (N, top_k) int32, weights (N, top_k) fp32): each token's top_k experts and their
+    softmax weights, over the chosen experts (renorm) or over all."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be (N, E)")
+    N, E = logits.shape
+    p = _dev(logits, torch.float32, "logits")
+    ids = _new((N, max(0, top_k)), torch.int32, logits.device, stream)
+    weights = _new((N, max(0, top_k)), torch.float32, logits.device, stream)
+    _check(lib.gq_moe_route(p, N, E, top_k, int(renorm), ids.data_ptr(), weights.data_ptr(),
+                            _call_stream(stream, logits)), "gq_moe_route")
+    return ids, weights
+
+
+class MoeExperts:
+    """The experts of one layer: gate and up (E * F rows of D weights) and down (E * D rows of F)
+    as uint8 CUDA tensors of blocks, types `t` and `t_down` (default: the same)."""
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, t, E: int, D: int,
+                 F: int, t_down=None):
+        t_down = t if t_down is None else t_down
+        for w, n, name in ((gate, E * F * row_bytes(t, D), "W_gate"),
+                           (up, E * F * row_bytes(t, D), "W_up"),
+                           (down, E * D * row_bytes(t_down, F), "W_down")):
+            _has(w, n, name)
+        self.E, self.D, self.F = E, D, F
+        self.tensors = (gate, up, down)   # kept alive: the struct holds raw pointers
+        self.c = Experts(_dev(gate, torch.uint8, "W_gate"), _dev(up, torch.uint8, "W_up"),
+                         _dev(down, torch.uint8, "W_down"), _type(t), _type(t_down), E, D, F)
+
+    def workspace_size(self, N: int, top_k: int) -> int:
+        return int(lib.gq_moe_workspace_size(ctypes.byref(self.c), N, top_k))
+
+
+def moe_swiglu(experts: MoeExperts, X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Y (N, D): the experts ids (N, top_k) of every token, weighted. With a `workspace` (uint8
+    CUDA tensor of experts.workspace_size(N, top_k) bytes) the call can be captured."""
+    X = _tokens(X, experts.D)
+    N = X.shape[0]
+    ids, weights = (ids.view(1, -1), weights.view(1, -1)) if ids.dim() == 1 else (ids, weights)
+    if ids.dim() != 2 or ids.shape[0] != N or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be (N, top_k)")
+    if out is None:
+        out = _new((N, experts.D), torch.float32, X.device, stream)
+    _has(out, N * experts.D, "Y")
+    args = (ctypes.byref(experts.c), _dev(X, torch.float32, "X"), N, _dev(ids, torch.int32, "ids"),
+            _dev(weights, torch.float32, "weights"), ids.shape[1], _dev(out, torch.float32, "Y"))
+    s = _call_stream(stream, X, ids, weights, out, experts.tensors[0])
+    if workspace is None:
+        _check(lib.gq_moe_swiglu(*args, s), "gq_moe_swiglu")
+    else:
+        _check(lib.gq_moe_swiglu_ws(*args, _dev(workspace, torch.uint8, "workspace"),
+                                    workspace.numel(), s), "gq_moe_swiglu_ws")
+    return out
 
 
 def get_last_error(stream=None) -> int:

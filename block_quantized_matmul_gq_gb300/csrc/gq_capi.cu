@@ -122,10 +122,33 @@ cudaError_t internal_workspace(cudaStream_t s, size_t bytes, void** out) {
     return cudaSuccess;
 }
 
+// The same for the calls whose graphs would keep the buffer's address: they are refused while
+// the stream is being captured (the buffer can be freed by a later, larger call and is shared
+// by every call on the stream, which a replayed graph does not respect). Their _ws forms are
+// the ones to capture.
+cudaError_t eager_workspace(cudaStream_t s, size_t bytes, void** out) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) return e;
+    if (cap != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
+    return internal_workspace(s, bytes, out);
+}
+
 // Runs one validated, non-empty problem (K > 0): tensor cores when the shape qualifies,
 // else the decode kernels. `ws` may be NULL (library workspace is used then).
 gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_t ws_bytes,
                   cudaStream_t s) {
+    if (t == GQ_TYPE_MXFP4) {
+        const size_t need = static_cast<size_t>(gq::few_workspace_bytes(p.K, N));
+        if (ws == nullptr) {
+            if (eager_workspace(s, need, &ws) != cudaSuccess) return GQ_ERR_CUDA;
+            ws_bytes = need;
+        } else if (ws_bytes < need || !aligned(ws, 256)) {
+            return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
+        }
+        return from_cuda(
+            gq::launch_few_mul_mat(p, N, ws, static_cast<int64_t>(ws_bytes), s));
+    }
     if (gq::gemv_tc_eligible(t, p, N)) {
         const size_t need = static_cast<size_t>(gq::gemv_tc_workspace_bytes(t, &p, 1, N));
         void* w = ws;
@@ -179,6 +202,11 @@ gq_status gq_quantize_q4_k(const float* W, int64_t M, int64_t K, void* W_blocks,
     return quantize_impl(GQ_TYPE_Q4_K, W, M, K, W_blocks, stream);
 }
 
+gq_status gq_quantize_mxfp4(const float* W, int64_t M, int64_t K, void* W_blocks,
+                            void* stream) {
+    return quantize_impl(GQ_TYPE_MXFP4, W, M, K, W_blocks, stream);
+}
+
 gq_status gq_dequantize(const void* W_blocks, gq_type t, int64_t M, int64_t K, float* W_out,
                         void* stream) {
     if (!known_type(t)) return GQ_ERR_TYPE;
@@ -205,6 +233,7 @@ gq_status gq_mul_mat(const void* W_blocks, gq_type t, int64_t M, int64_t K, cons
 size_t gq_mul_mat_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N) {
     if (!known_type(t) || check_shape(t, M, K, N) != GQ_OK || M == 0 || N == 0 || K == 0)
         return 0;
+    if (t == GQ_TYPE_MXFP4) return static_cast<size_t>(gq::few_workspace_bytes(K, N));
     gq::MatProblem p{reinterpret_cast<const uint8_t*>(uintptr_t(256)),
                      reinterpret_cast<const float*>(uintptr_t(256)), nullptr, M, K};
     if (gq::gemv_tc_eligible(t, p, N))
@@ -221,7 +250,8 @@ gq_status gq_mul_mat_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K, c
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
     gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
-    if ((gq::gemm_eligible(t, p, N) || gq::gemv_tc_eligible(t, p, N)) && workspace == nullptr)
+    if ((t == GQ_TYPE_MXFP4 || gq::gemm_eligible(t, p, N) || gq::gemv_tc_eligible(t, p, N)) &&
+        workspace == nullptr)
         return GQ_ERR_NULL;
     return run_one(t, p, N, workspace, workspace_bytes, s);
 }
@@ -234,7 +264,7 @@ namespace {
 // problems; K == 0 ones are zeroed on the stream here.
 struct BatchPlan {
     gq::MatProblem gemm[GQ_MAX_BATCH], tc[GQ_MAX_BATCH], cc[GQ_MAX_BATCH];
-    int n_gemm = 0, n_tc = 0, n_cc = 0;
+    int n_gemm = 0, n_tc = 0, n_cc = 0;   // MXFP4 problems run one by one, as gemm ones do
     size_t ws_bytes = 0;   // max(largest GEMM workspace, sum of tensor-core decode tiles)
 };
 
@@ -260,7 +290,10 @@ gq_status plan_batch(const gq_mul_mat_problem* problems, int32_t count, gq_type 
             continue;
         }
         const gq::MatProblem mp{static_cast<const uint8_t*>(p.W_blocks), p.X, p.Y, p.M, p.K};
-        if (gq::gemm_eligible(t, mp, N)) {
+        if (t == GQ_TYPE_MXFP4) {
+            plan->gemm[plan->n_gemm++] = mp;
+            gemm_max = std::max(gemm_max, static_cast<size_t>(gq::few_workspace_bytes(p.K, N)));
+        } else if (gq::gemm_eligible(t, mp, N)) {
             plan->gemm[plan->n_gemm++] = mp;
             gemm_max = std::max(gemm_max, static_cast<size_t>(gq::gemm_workspace_bytes(p.K, N)));
         } else if (gq::gemv_tc_eligible(t, mp, N)) {
@@ -281,15 +314,19 @@ gq_status run_batch(gq_type t, int64_t N, BatchPlan* plan, void* ws, size_t ws_b
                     cudaStream_t s) {
     if (plan->ws_bytes > 0) {
         if (ws == nullptr) {
-            if (internal_workspace(s, plan->ws_bytes, &ws) != cudaSuccess) return GQ_ERR_CUDA;
+            const cudaError_t e = t == GQ_TYPE_MXFP4 ? eager_workspace(s, plan->ws_bytes, &ws)
+                                                     : internal_workspace(s, plan->ws_bytes, &ws);
+            if (e != cudaSuccess) return GQ_ERR_CUDA;
             ws_bytes = plan->ws_bytes;
         } else if (ws_bytes < plan->ws_bytes || !aligned(ws, 256)) {
             return ws_bytes < plan->ws_bytes ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
         }
     }
     for (int i = 0; i < plan->n_gemm; ++i) {
-        gq_status st = from_cuda(
-            gq::launch_gemm(t, plan->gemm[i], N, ws, static_cast<int64_t>(ws_bytes), s));
+        gq_status st = t == GQ_TYPE_MXFP4
+                           ? run_one(t, plan->gemm[i], N, ws, ws_bytes, s)
+                           : from_cuda(gq::launch_gemm(t, plan->gemm[i], N, ws,
+                                                       static_cast<int64_t>(ws_bytes), s));
         if (st != GQ_OK) return st;
     }
     if (plan->n_tc > 0) {
@@ -314,7 +351,8 @@ gq_status check_q8x(const void* W, gq_type t, int64_t M, int64_t K, const float*
                     float* Y, cudaStream_t s, bool zero_k0, bool* run) {
     bool empty = false;
     *run = false;
-    if (t == GQ_TYPE_Q4_K) return GQ_ERR_TYPE;   // Q8_0 activation blocks pair with 32-weight blocks
+    // Q8_0 activation blocks pair with 32-weight integer blocks
+    if (t == GQ_TYPE_Q4_K || t == GQ_TYPE_MXFP4) return GQ_ERR_TYPE;
     gq_status st = check_problem(W, t, M, K, X, N, Y, &empty);
     if (st != GQ_OK || empty) return st;
     if (K == 0) {
@@ -354,7 +392,9 @@ gq_status gq_mul_mat_rmsnorm(const void* W_blocks, gq_type t, int64_t M, int64_t
     const size_t xb = (static_cast<size_t>(N * K) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     void* w = nullptr;
-    if (internal_workspace(s, xb + down, &w) != cudaSuccess) return GQ_ERR_CUDA;
+    if ((t == GQ_TYPE_MXFP4 ? eager_workspace(s, xb + down, &w)
+                            : internal_workspace(s, xb + down, &w)) != cudaSuccess)
+        return GQ_ERR_CUDA;
     float* xhat = static_cast<float*>(w);
     cudaError_t e = gq::launch_rmsnorm_x(X, gamma, eps, N, K, xhat, s);
     if (e != cudaSuccess) return GQ_ERR_CUDA;
@@ -379,7 +419,9 @@ gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int
     const size_t yb = (static_cast<size_t>(N * M) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     void* w = nullptr;
-    if (internal_workspace(s, 2 * yb + down, &w) != cudaSuccess) return GQ_ERR_CUDA;
+    if ((t == GQ_TYPE_MXFP4 ? eager_workspace(s, 2 * yb + down, &w)
+                            : internal_workspace(s, 2 * yb + down, &w)) != cudaSuccess)
+        return GQ_ERR_CUDA;
     float* G = static_cast<float*>(w);
     float* U = reinterpret_cast<float*>(static_cast<uint8_t*>(w) + yb);
     void* dws = static_cast<uint8_t*>(w) + 2 * yb;
@@ -404,7 +446,7 @@ gq_status gq_mul_mat_q8x(const void* W_blocks, gq_type t, int64_t M, int64_t K, 
 gq_status gq_mul_mat_q8x_batched(const gq_mul_mat_problem* problems, int32_t count, gq_type t,
                                  int64_t N, void* stream) {
     if (count < 0 || count > GQ_MAX_BATCH) return GQ_ERR_SHAPE;
-    if (!known_type(t) || t == GQ_TYPE_Q4_K) return GQ_ERR_TYPE;
+    if (!known_type(t) || t == GQ_TYPE_Q4_K || t == GQ_TYPE_MXFP4) return GQ_ERR_TYPE;
     if (count == 0) return GQ_OK;
     if (!problems) return GQ_ERR_NULL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -451,6 +493,131 @@ gq_status gq_mul_mat_batched_ws(const gq_mul_mat_problem* problems, int32_t coun
     if (st != GQ_OK) return st;
     if (plan.ws_bytes > 0 && workspace == nullptr) return GQ_ERR_NULL;
     return run_batch(t, N, &plan, workspace, workspace_bytes, s);
+}
+
+size_t gq_mul_mat_mx4x_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N) {
+    if (t != GQ_TYPE_MXFP4 || check_shape(t, M, K, N) != GQ_OK || M == 0 || N == 0 || K == 0)
+        return 0;
+    return static_cast<size_t>(gq::mx4x_workspace_bytes(M, K, N));
+}
+
+gq_status gq_mul_mat_mx4x_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K,
+                             const float* X, int64_t N, float* Y, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    if (t != GQ_TYPE_MXFP4) return GQ_ERR_TYPE;   // both operands are microscaled
+    bool empty = false;
+    gq_status st = check_problem(W_blocks, t, M, K, X, N, Y, &empty);
+    if (st != GQ_OK || empty) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
+    if (!workspace) return GQ_ERR_NULL;
+    if (workspace_bytes < gq_mul_mat_mx4x_workspace_size(t, M, K, N)) return GQ_ERR_SHAPE;
+    if (!aligned(workspace, 256)) return GQ_ERR_ALIGN;
+    const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
+    return from_cuda(gq::launch_mx4x(p, N, workspace, s));
+}
+
+gq_status gq_mul_mat_mx4x(const void* W_blocks, gq_type t, int64_t M, int64_t K, const float* X,
+                          int64_t N, float* Y, void* stream) {
+    if (t != GQ_TYPE_MXFP4) return GQ_ERR_TYPE;
+    bool empty = false;
+    gq_status st = check_problem(W_blocks, t, M, K, X, N, Y, &empty);
+    if (st != GQ_OK || empty) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
+    void* w = nullptr;
+    if (eager_workspace(s, gq_mul_mat_mx4x_workspace_size(t, M, K, N), &w) != cudaSuccess)
+        return GQ_ERR_CUDA;
+    const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
+    return from_cuda(gq::launch_mx4x(p, N, w, s));
+}
+
+gq_status gq_moe_route(const float* logits, int64_t N, int64_t E, int32_t top_k, int32_t renorm,
+                       int32_t* ids, float* weights, void* stream) {
+    if (N < 0 || N > kMaxDim || E < 1 || E > gq::kMoeMaxExperts) return GQ_ERR_SHAPE;
+    if (top_k < 1 || top_k > E || top_k > gq::kMoeMaxTopK) return GQ_ERR_SHAPE;
+    if (N == 0) return GQ_OK;
+    if (!logits || !ids || !weights) return GQ_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return GQ_ERR_ALIGN;
+    return from_cuda(gq::launch_moe_route(logits, N, static_cast<int>(E), top_k, renorm != 0, ids,
+                                          weights, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks a mixture-of-experts call; *run tells whether anything is to be computed.
+gq_status check_moe(const gq_moe_experts* x, const float* X, int64_t N, const int32_t* ids,
+                    const float* weights, int32_t top_k, float* Y, gq::MoeProblem* m,
+                    bool* run) {
+    *run = false;
+    if (!x) return GQ_ERR_NULL;
+    if (!known_type(x->type) || !known_type(x->down_type)) return GQ_ERR_TYPE;
+    if (x->E < 1 || x->E > gq::kMoeMaxExperts || x->D < 1 || x->F < 1) return GQ_ERR_SHAPE;
+    if (top_k < 1 || top_k > gq::kMoeMaxTopK) return GQ_ERR_SHAPE;
+    if (x->D > kMaxDim || x->F > kMaxDim || x->E * x->F > kMaxDim || x->E * x->D > kMaxDim)
+        return GQ_ERR_SHAPE;
+    // both widths are a K of one product and the rows of another
+    if (check_shape(x->type, x->E * x->F, x->D, N) != GQ_OK ||
+        check_shape(x->down_type, x->E * x->D, x->F, N) != GQ_OK)
+        return GQ_ERR_SHAPE;
+    if (x->D % 32 != 0 || x->F % 32 != 0) return GQ_ERR_SHAPE;
+    if (N == 0) return GQ_OK;
+    if (!x->W_gate || !x->W_up || !x->W_down || !X || !ids || !weights || !Y) return GQ_ERR_NULL;
+    if (!aligned(x->W_gate, 16) || !aligned(x->W_up, 16) || !aligned(x->W_down, 16) ||
+        !aligned(X, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(Y, 4))
+        return GQ_ERR_ALIGN;
+    *m = {static_cast<const uint8_t*>(x->W_gate), static_cast<const uint8_t*>(x->W_up),
+          static_cast<const uint8_t*>(x->W_down), x->type, x->down_type, x->E, x->D, x->F, N,
+          top_k, X, ids, weights, Y};
+    *run = true;
+    return GQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gq_moe_workspace_size(const gq_moe_experts* experts, int64_t N, int32_t top_k) {
+    if (!experts) return 0;
+    float* const any = reinterpret_cast<float*>(uintptr_t(256));   // only the sizes count
+    gq_moe_experts x = *experts;
+    x.W_gate = x.W_up = x.W_down = any;
+    gq::MoeProblem m{};
+    bool run = false;
+    if (check_moe(&x, any, N, reinterpret_cast<const int32_t*>(any), any, top_k, any, &m, &run) !=
+            GQ_OK ||
+        !run)
+        return 0;
+    return static_cast<size_t>(gq::moe_workspace_bytes(m));
+}
+
+gq_status gq_moe_swiglu_ws(const gq_moe_experts* experts, const float* X, int64_t N,
+                           const int32_t* ids, const float* weights, int32_t top_k, float* Y,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    gq::MoeProblem m{};
+    bool run = false;
+    const gq_status st = check_moe(experts, X, N, ids, weights, top_k, Y, &m, &run);
+    if (st != GQ_OK || !run) return st;
+    if (!workspace) return GQ_ERR_NULL;
+    if (workspace_bytes < static_cast<size_t>(gq::moe_workspace_bytes(m))) return GQ_ERR_SHAPE;
+    if (!aligned(workspace, 256)) return GQ_ERR_ALIGN;
+    return from_cuda(gq::launch_moe(m, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+gq_status gq_moe_swiglu(const gq_moe_experts* experts, const float* X, int64_t N,
+                        const int32_t* ids, const float* weights, int32_t top_k, float* Y,
+                        void* stream) {
+    gq::MoeProblem m{};
+    bool run = false;
+    const gq_status st = check_moe(experts, X, N, ids, weights, top_k, Y, &m, &run);
+    if (st != GQ_OK || !run) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* w = nullptr;
+    if (eager_workspace(s, static_cast<size_t>(gq::moe_workspace_bytes(m)), &w) != cudaSuccess)
+        return GQ_ERR_CUDA;
+    return from_cuda(gq::launch_moe(m, w, s));
 }
 
 gq_status gq_get_last_error(void* stream) {

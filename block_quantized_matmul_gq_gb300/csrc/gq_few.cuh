@@ -1,0 +1,81 @@
+// gq_few.cuh -- what the few-token kernels (gq_few.cu) and their callers share: the split
+// activation format, its element order, and the launchers.
+//
+// Split activations. One 32-element block of one activation row becomes
+//   2 x 32 fp16   hi and lo with x = 2^(e - 14) (hi + lo), e = floor(log2 max |x|): the block
+//                 maximum lands in [2^14, 2^15), so hi keeps 11 significant bits and lo the
+//                 next 11 of every element down to 2^-38 of the block maximum;
+//   one float2    {scale 2^(e - 14), the block's sum (Q4_K's mins multiply it)}.
+// The weights enter the tensor cores as exact fp16 integers (or E2M1 values), so a product's
+// only rounding beside the fp32 sums is the 2^-22 of hi + lo.
+//
+// MXFP4 activations (the microscaled product) use one term: the E2M1 values themselves, and
+// one float 2^e per block.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "gq_device.cuh"
+#include "gq_internal.h"
+
+namespace gq {
+
+constexpr int kFewGroup2 = 16;    // tokens per pass over the weights, two-term activations
+constexpr int kFewGroup1 = 32;    // one-term activations
+
+// Place (0..31) of element i of a block in the order in which the four lanes that share a
+// weight row hold it: lane t = place / 8 takes the block's bytes 4t..4t+3 (and 16 + 4t.. for
+// the types with 32 code bytes), and the shifts and masks that unpack a word of codes yield
+// pairs in these orders. The contraction does not depend on the order, so activations are
+// stored in the weights' order and no weight is ever moved between lanes.
+__host__ __device__ __forceinline__ int few_place(int type, int i) {
+    const int t = (i & 15) >> 2, r = i & 3, hi = i >> 4;
+    int slot;
+    if (type == GQ_TYPE_MXFP4)
+        slot = 2 * r + hi;                                  // byte r: (low, high) nibbles
+    else if (type == GQ_TYPE_Q8_0)
+        slot = r + 4 * hi;                                  // four bytes of each word
+    else if (type == GQ_TYPE_Q4_0)
+        slot = 2 * (2 * (r & 1) + hi) + (r >> 1);           // masks 0x000F000F << 0, 4, 8, 12
+    else
+        slot = 2 * (2 * hi + (r & 1)) + (r >> 1);           // Q4_K: one nibble of each word
+    return 8 * t + slot;
+}
+
+// Exponent e (clamped so that 2^(14 - e) and 2^(e - 14) are normal) of a block maximum given
+// as the bits of a non-negative float.
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
+    const int e = static_cast<int>(amax_bits >> 23) - 127;
+    return e < -110 ? -110 : (e > 127 ? 127 : e);
+}
+
+__device__ __forceinline__ float pow2f(int e) {   // e in [-126, 127]
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// E2M1 code (0..7) of a magnitude already divided by its block scale: nearest value, ties to
+// the even code, above 6 saturates.
+__device__ __forceinline__ uint32_t e2m1_code(float a) {
+    return (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) +
+           (a > 5.0f);
+}
+
+// E8M0 scale byte of a block maximum (bits of a non-negative float): floor(log2 amax) - 2 with
+// bias 127, 0 for a zero (or smaller) block, 255 (NaN) for a block with an infinity or a NaN.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+    const uint32_t e = amax_bits >> 23;
+    return e == 255 ? 255 : (e > 2 ? e - 2 : 0);
+}
+
+// 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+    return __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255 ? 0x7FC00000u : byte << 23));
+}
+
+// 2^(127 - byte) for byte <= 254.
+__device__ __forceinline__ float mx_inverse_scale(uint32_t byte) {
+    return byte == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((254u - byte) << 23);
+}
+
+}  // namespace gq

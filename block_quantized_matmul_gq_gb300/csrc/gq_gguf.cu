@@ -73,6 +73,7 @@ TypeSize type_size(uint32_t t) {
         case 27: return {1, 8};     // I64
         case 28: return {1, 8};     // F64
         case 30: return {1, 2};     // BF16
+        case 39: return {32, 17};   // MXFP4
         default: return {0, 0};
     }
 }
@@ -336,7 +337,7 @@ gq_status gq_gguf_tensor_matrix(const gq_gguf* f, int64_t i, gq_type* type, int6
     if (!f || !type || !M || !K) return GQ_ERR_NULL;
     if (bad_tensor(f, i)) return GQ_ERR_SHAPE;
     const Tensor& t = f->tensors[static_cast<size_t>(i)];
-    const gq_type gt = static_cast<gq_type>(t.type);   // the three block ids coincide
+    const gq_type gt = static_cast<gq_type>(t.type);   // the block ids coincide
     if (gq::block_bytes_of(gt) == 0) return GQ_ERR_TYPE;
     if (t.ne[2] != 1 || t.ne[3] != 1) return GQ_ERR_SHAPE;
     *type = gt;

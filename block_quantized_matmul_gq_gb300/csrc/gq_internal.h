@@ -13,12 +13,14 @@ constexpr int kQ4Bytes = 18;    // fp16 scale + 16 bytes of nibble codes
 constexpr int kQ8Bytes = 34;    // fp16 scale + 32 int8 codes
 constexpr int kQ4KBytes = 144;  // Q4_K super-block: fp16 d, fp16 dmin, 12 scale bytes, 128 code bytes
 constexpr int kQ4KWeights = 256;
+constexpr int kMxfp4Bytes = 17;  // E8M0 scale + 16 bytes of E2M1 codes
 
 inline int block_bytes_of(gq_type t) {
     switch (t) {
         case GQ_TYPE_Q4_0: return kQ4Bytes;
         case GQ_TYPE_Q8_0: return kQ8Bytes;
         case GQ_TYPE_Q4_K: return kQ4KBytes;
+        case GQ_TYPE_MXFP4: return kMxfp4Bytes;
     }
     return 0;
 }
@@ -100,5 +102,38 @@ bool gemv_tc_eligible(gq_type t, const MatProblem& p, int64_t N);
 int64_t gemv_tc_workspace_bytes(gq_type t, const MatProblem* probs, int count, int64_t N);
 cudaError_t launch_gemv_tc(gq_type t, const MatProblem* probs, int count, int64_t N,
                            void* workspace, cudaStream_t s);
+
+// A few tokens to fp32 accuracy (gq_few.cu): MXFP4 mul_mat with fp32 X, the same with X
+// quantized to MXFP4, and the mixture-of-experts layer. Workspaces 256-byte aligned.
+// launch_few_mul_mat takes its tokens in as many passes as the workspace makes necessary.
+int64_t few_workspace_bytes(int64_t K, int64_t N);
+int64_t few_tokens_that_fit(int64_t M, int64_t K, int64_t N, int64_t workspace_bytes);
+cudaError_t launch_few_mul_mat(const MatProblem& p, int64_t N, void* workspace,
+                               int64_t workspace_bytes, cudaStream_t s);
+int64_t few_mx_workspace_bytes(int64_t K, int64_t N);
+cudaError_t launch_few_mx4x(const MatProblem& p, int64_t N, void* workspace, cudaStream_t s);
+// X quantized to MXFP4, any N (gq_mx.cu chooses the kernel).
+int64_t mx4x_workspace_bytes(int64_t M, int64_t K, int64_t N);
+cudaError_t launch_mx4x(const MatProblem& p, int64_t N, void* workspace, cudaStream_t s);
+
+constexpr int kMoeMaxPairs = 512;      // (token, expert) pairs of one launch
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopK = 64;
+
+struct MoeProblem {   // validated, N > 0, D > 0, F > 0, E > 0, top_k > 0
+    const uint8_t *W_gate, *W_up, *W_down;
+    gq_type t, t_down;
+    int64_t E, D, F, N;
+    int top_k;
+    const float* X;
+    const int32_t* ids;
+    const float* weights;
+    float* Y;
+};
+int64_t moe_workspace_bytes(const MoeProblem& m);
+cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s);
+// Router: the top_k experts of each token and their softmax weights (gq_moe.cu).
+cudaError_t launch_moe_route(const float* logits, int64_t N, int E, int top_k, bool renorm,
+                             int32_t* ids, float* weights, cudaStream_t s);
 
 }  // namespace gq

@@ -77,6 +77,12 @@ extern "C" gq_status gq_mul_mat_noalloc(const void* W_blocks, gq_type t, int64_t
                                                                             : GQ_ERR_CUDA;
     const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
     const int64_t cap = static_cast<int64_t>(gq::kNoAllocScratchBytes);
+    if (t == GQ_TYPE_MXFP4) {   // as many tokens a pass as the array holds split
+        if (gq::few_tokens_that_fit(M, K, N, cap) < 1) return GQ_ERR_SHAPE;
+        void* scratch = nullptr;
+        if (gq::noalloc_scratch(&scratch) != cudaSuccess) return GQ_ERR_CUDA;
+        return gq::launch_few_mul_mat(p, N, scratch, cap, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    }
     // Tensor-core decode (3..64 tokens): its bf16 X tiles, partial sums and split-tile
     // counters fit the array for any K up to ~390k; x_tiles_kernel rewrites the tiles and
     // zeroes the counters at the start of every call. Past that size, the CUDA-core decode

@@ -1,8 +1,8 @@
 """GGUF files through libgq's reader (include/gq_gguf.h): argument marshalling only.
 
 The file is memory-mapped and parsed by the library; this module turns its answers into
-Python values and copies tensors to the device with gq_gguf_upload. A Q4_0 / Q8_0 / Q4_K
-weight matrix arrives as an (M, row_bytes) uint8 CUDA tensor that binding.mul_mat takes
+Python values and copies tensors to the device with gq_gguf_upload. A Q4_0 / Q8_0 / Q4_K /
+MXFP4 weight matrix arrives as an (M, row_bytes) uint8 CUDA tensor that binding.mul_mat takes
 as it is.
 """
 from __future__ import annotations
@@ -20,7 +20,8 @@ UINT8, INT8, UINT16, INT16, UINT32, INT32, FLOAT32, BOOL, STRING, ARRAY, UINT64,
     FLOAT64 = range(13)
 _NUMPY = {UINT8: "<u1", INT8: "<i1", UINT16: "<u2", INT16: "<i2", UINT32: "<u4", INT32: "<i4",
           FLOAT32: "<f4", BOOL: "<u1", UINT64: "<u8", INT64: "<i8", FLOAT64: "<f8"}
-_BLOCK_TYPES = {binding.Q4_0: "q4_0", binding.Q8_0: "q8_0", binding.Q4_K: "q4_k"}
+_BLOCK_TYPES = {binding.Q4_0: "q4_0", binding.Q8_0: "q8_0", binding.Q4_K: "q4_k",
+                binding.MXFP4: "mxfp4"}
 
 
 @dataclass(frozen=True)

@@ -1,5 +1,5 @@
 /*
- * gq.h -- C ABI of libgq: block-quantized (Q4_0 / Q8_0 / Q4_K) weights times fp32
+ * gq.h -- C ABI of libgq: block-quantized (Q4_0 / Q8_0 / Q4_K / MXFP4) weights times fp32
  * activations on one NVIDIA GB300 GPU (sm_103a). Reading such weights out of GGUF files:
  * gq_gguf.h.
  *
@@ -23,6 +23,7 @@
  *       Q8_0, 34 bytes: fp16 scale d, then 32 signed bytes c; What = c * d.
  *       Q4_K, 144-byte super-blocks of 256 weights, K/256 per row (layout at
  *             gq_quantize_q4_k).
+ *       MXFP4, 17 bytes per 32 weights (layout at gq_quantize_mxfp4).
  *   - Pointers. Every array pointer is owned by the caller; the library keeps none of them
  *     after the call returns. W_blocks and workspaces are DEVICE pointers. X, Y (and the
  *     fused forms' gamma and H) are device pointers or pointers to page-locked host memory
@@ -72,7 +73,8 @@ extern "C" {
 typedef enum gq_type {
     GQ_TYPE_Q4_0 = 2,   /* 18-byte blocks: fp16 scale + 32 4-bit codes */
     GQ_TYPE_Q8_0 = 8,   /* 34-byte blocks: fp16 scale + 32 int8 codes */
-    GQ_TYPE_Q4_K = 12   /* 144-byte super-blocks of 256 weights (layout below) */
+    GQ_TYPE_Q4_K = 12,  /* 144-byte super-blocks of 256 weights (layout below) */
+    GQ_TYPE_MXFP4 = 39  /* 17-byte blocks: E8M0 scale byte + 32 E2M1 codes (layout below) */
 } gq_type;
 
 typedef enum gq_status {
@@ -91,8 +93,8 @@ typedef enum gq_status {
 /* Version of this ABI (GQ_ABI_VERSION of the header the library was built with). */
 int32_t gq_abi_version(void);
 
-/* Bytes of one block: 18 (Q4_0) or 34 (Q8_0) per 32 weights, 144 (Q4_K) per 256; 0 for
- * an unknown type. */
+/* Bytes of one block: 18 (Q4_0), 34 (Q8_0) or 17 (MXFP4) per 32 weights, 144 (Q4_K) per 256;
+ * 0 for an unknown type. */
 size_t gq_block_bytes(gq_type t);
 
 /* Bytes of one quantized row of K weights: (K / 32) * gq_block_bytes(t), or for Q4_K
@@ -156,8 +158,33 @@ gq_status gq_quantize_q4_k(const float* W, int64_t M, int64_t K, void* W_blocks,
                            void* stream);
 
 /*
- * Expand blocks back to fp32: W_out[m][k] = (c - 8) * d (Q4_0), c * d (Q8_0), or
- * d sc_j q - dmin m_j (Q4_K), exact up to Q4_K's one rounding ("Development Guide ...",
+ * MXFP4 blocks: the microscaled 4-bit floating point of the OCP MX specification, 32 weights,
+ * 17 bytes, in GGUF's arrangement:
+ *   byte 0       s, the shared scale 2^(s - 127) (E8M0); 255 is NaN
+ *   bytes 1-16   E2M1 codes c; byte 1 + j holds weight j (low nibble) and j + 16 (high nibble);
+ *                bit 3 is the sign, bits 0-2 a magnitude of {0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ *   What = 2^(s - 127) E2M1(c), exact in fp32.
+ * Conversion: e = floor(log2 max |w|) - 2, not below -127 (which an all-zero block gets, too);
+ * c = the E2M1 value nearest to w / 2^e, ties to the even code, 6 where it is above 6. A block
+ * with an infinity or a NaN gets s = 255 and codes 0: all its weights read back as NaN.
+ * Bit-for-bit reproducible. K must be a multiple of 32; K and M are otherwise free.
+ * The mul_mat entry points take MXFP4 for every N, to fp32 accuracy (X is split in two fp16
+ * terms, 22 bits): |Y - Y_exact| <= (K / 32 + 160) 2^-24 sum_k |What[m][k] X[n][k]|, the
+ * roundings of X's terms and of the fp32 sums. Each needs a
+ * workspace (gq_mul_mat_workspace_size); the forms that use the library's refuse to be captured
+ * into a graph (GQ_ERR_CUDA), the _ws forms and gq_mul_mat_noalloc do not. gq_mul_mat_batched
+ * runs MXFP4 problems one after another. gq_mul_mat_rmsnorm and gq_mul_mat_swiglu take it in
+ * their composite forms; gq_mul_mat_q8x does not (GQ_ERR_TYPE; gq_mul_mat_mx4x is its kind).
+ * Range: where |X| / 2^e' of a block (e' as e above) and 2^(s - 127) are so far apart that a
+ * product leaves fp32's normal range, it is rounded as fp32 is. Non-finite values of a token
+ * reach that token's results alone.
+ */
+gq_status gq_quantize_mxfp4(const float* W, int64_t M, int64_t K, void* W_blocks,
+                            void* stream);
+
+/*
+ * Expand blocks back to fp32: W_out[m][k] = (c - 8) * d (Q4_0), c * d (Q8_0),
+ * 2^(s - 127) E2M1(c) (MXFP4), or d sc_j q - dmin m_j (Q4_K), exact up to Q4_K's one rounding ("Development Guide ...",
  * section 6.2, the unpack and dequantize steps). W_out receives M x K floats.
  */
 gq_status gq_dequantize(const void* W_blocks, gq_type t, int64_t M, int64_t K,
@@ -192,7 +219,9 @@ gq_status gq_mul_mat(const void* W_blocks, gq_type t, int64_t M, int64_t K,
  * P = 16, 32 or 64 token rows of pre-arranged bf16 X (Q4_K with N <= 16: plus K / 256 * 1024
  * for the X block sums), plus 2 * 256 * 128 * P * 4 + 4096 for the partial sums (and
  * their counters) of tiles whose k range is split between CTAs;
- * N * K * 2 (a bf16 copy of X, rounded up to 256) on the prefill path (N >= 65).
+ * N * K * 2 (a bf16 copy of X, rounded up to 256) on the prefill path (N >= 65). MXFP4, for
+ * every N: N' * K * 4 + N' * K / 4 for the split X of N' = min(N, 4096) tokens (each part
+ * rounded up to 256).
  * Tensor-core paths need K a multiple of 256. 0 for invalid arguments.
  */
 size_t gq_mul_mat_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N);
@@ -226,6 +255,8 @@ gq_status gq_mul_mat_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K,
  *     exceeds 64 MiB (N * K > 32 Mi) return GQ_ERR_SHAPE;
  *   - the tensor-core decode (3 <= N <= 64) needs at most 64 * K * 2 bytes + 16 MiB + 4 KiB
  *     there; a larger K (beyond ~390k) runs on the CUDA-core decode kernels instead;
+ *   - MXFP4 takes its tokens in as many passes as the array makes necessary (4.25 K bytes a
+ *     token; GQ_ERR_SHAPE when one token does not fit);
  *   - the first call on a device looks up that array's device address (a one-time host-side
  *     set-up). The address is kept for the life of the process, so libgq must not be used
  *     again on a device the process has reset with cudaDeviceReset;
@@ -332,6 +363,80 @@ gq_status gq_mul_mat_rmsnorm(const void* W_blocks, gq_type t, int64_t M, int64_t
                              float* Y, void* stream);
 gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int64_t M,
                             int64_t K, const float* X, int64_t N, float* H, void* stream);
+
+/*
+ * Microscaled mul_mat: both operands MXFP4. Every 32-element block of each X row is quantized
+ * as gq_quantize_mxfp4 does, and Y = Xhat . What^T: products exact, sums in fp32. Like
+ * gq_mul_mat_q8x an approximation that the caller opts into (E2M1 keeps two significant bits);
+ * against its own definition the error is that of the fp32 sums, at most
+ * (K / 32 + 160) 2^-24 sum_k |What[m][k] Xhat[n][k]|. With many
+ * tokens it runs on the block-scaled tensor cores, which take MXFP4 operands as they are.
+ * t must be GQ_TYPE_MXFP4 (else GQ_ERR_TYPE); other arguments as gq_mul_mat; any N. An X block
+ * with an infinity or a NaN makes its token's results NaN.
+ * gq_mul_mat_mx4x uses the library's workspace (refused while the stream is captured,
+ * GQ_ERR_CUDA); gq_mul_mat_mx4x_ws the caller's: 256-byte aligned, at least
+ * gq_mul_mat_mx4x_workspace_size bytes (0 for invalid or empty arguments), used by no other
+ * work in flight; it allocates nothing and can be captured. GQ_ERR_NULL / _SHAPE / _ALIGN for a
+ * missing, small or misaligned one.
+ */
+gq_status gq_mul_mat_mx4x(const void* W_blocks, gq_type t, int64_t M, int64_t K,
+                          const float* X, int64_t N, float* Y, void* stream);
+size_t gq_mul_mat_mx4x_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N);
+gq_status gq_mul_mat_mx4x_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K,
+                             const float* X, int64_t N, float* Y, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Mixture of experts: a feed-forward layer of E gated networks of which each token uses top_k.
+ *
+ * gq_moe_route: the router's choice. logits: N x E fp32. Per token the top_k experts with the
+ * largest logits, largest first, equal ones by lower index, into ids (N x top_k int32), and
+ * their softmax weights into weights (N x top_k fp32):
+ *     p_e = exp(z_e - max z) / sum_e' exp(z_e' - max z), the sum over all experts, or with
+ *     renorm != 0 over the chosen ones (the weights then add up to 1).
+ * A logit of -infinity (or NaN) masks its expert: it comes last and weighs 0; a token with
+ * every expert masked gets ids 0 .. top_k - 1 with weights 0. Experts at +infinity share the
+ * weight. 1 <= top_k <= min(E, 64), E <= 1024 (else GQ_ERR_SHAPE); all arrays 4-byte aligned.
+ */
+gq_status gq_moe_route(const float* logits, int64_t N, int64_t E, int32_t top_k, int32_t renorm,
+                       int32_t* ids, float* weights, void* stream);
+
+/* The experts of one layer: E matrices one after another in each array (16-byte aligned, as
+ * one E * rows x K matrix of gq_mul_mat). */
+typedef struct gq_moe_experts {
+    const void* W_gate;   /* E x F rows of D weights */
+    const void* W_up;     /* E x F rows of D weights */
+    const void* W_down;   /* E x D rows of F weights */
+    gq_type type;         /* of W_gate and W_up: any of the four block types */
+    gq_type down_type;    /* of W_down */
+    int64_t E, D, F;      /* experts, model width, expert width */
+} gq_moe_experts;
+
+/*
+ * gq_moe_swiglu: the whole layer behind the router, for a few tokens:
+ *     Y[n] = sum_j weights[n][j] * Wdown_e ( Swish(Wgate_e X[n]) (.) Wup_e X[n] ),
+ *     e = ids[n][j], j = 0 .. top_k - 1 in this order.
+ *   - X: N x D, ids and weights: N x top_k, Y: N x D (device pointers; the struct is read on
+ *     the host during the call). Y must not overlap the other arrays.
+ *   - An id outside [0, E) stands for no expert (padding): its weight is not read into the sum.
+ *     A token without any gets Y[n] = 0. The same id twice counts twice.
+ *   - D and F: multiples of 32, and of 256 where type (D) or down_type (F) is Q4_K; E <= 1024;
+ *     1 <= top_k <= 64 (else GQ_ERR_SHAPE). Any N; N * top_k <= 512 runs in one pass over
+ *     the chosen experts' weights (three launches), more in several.
+ *   - Accuracy: fp32. X and the hidden vector are split in two fp16 terms (22 bits) and every
+ *     sum is held in fp32: each product's error is at most (K / 32 + 160) 2^-24
+ *     sum_k (|What| + |z|) |x|, z = dmin m for Q4_K (0 for the other types), carried on as in gq_mul_mat_swiglu. Results are deterministic.
+ *   - Only the weights of chosen experts are read, once per group of up to 16 tokens.
+ * Workspaces as for gq_mul_mat_mx4x: gq_moe_swiglu uses the library's (not in a capture),
+ * gq_moe_swiglu_ws the caller's gq_moe_workspace_size bytes.
+ */
+gq_status gq_moe_swiglu(const gq_moe_experts* experts, const float* X, int64_t N,
+                        const int32_t* ids, const float* weights, int32_t top_k, float* Y,
+                        void* stream);
+size_t gq_moe_workspace_size(const gq_moe_experts* experts, int64_t N, int32_t top_k);
+gq_status gq_moe_swiglu_ws(const gq_moe_experts* experts, const float* X, int64_t N,
+                           const int32_t* ids, const float* weights, int32_t top_k, float* Y,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Device-side status of the current device: synchronizes `stream`, then returns and

@@ -20,7 +20,7 @@
  *               start of the data section, a multiple of the alignment)
  *   data        starts at the first multiple of the alignment after the last tensor
  *               info; the alignment is the uint32 metadata "general.alignment", else 32.
- * The ggml type ids of the three block formats equal gq_type: 2 Q4_0, 8 Q8_0, 12 Q4_K, and
+ * The ggml type ids of the block formats equal gq_type: 2 Q4_0, 8 Q8_0, 12 Q4_K, 39 MXFP4, and
  * a 2-D weight tensor of those types is stored exactly as gq_mul_mat reads W_blocks:
  * M = ne[1] rows of gq_row_bytes(type, K = ne[0]) bytes each. So a tensor goes from the
  * file to the GPU with one copy and no conversion.
@@ -96,7 +96,7 @@ const void* gq_gguf_tensor_data(const gq_gguf* f, int64_t i);
 
 /*
  * A 2-D tensor of a block type that gq_mul_mat takes, as gq_mul_mat's arguments:
- * *type (GQ_TYPE_Q4_0, _Q8_0 or _Q4_K), *M = ne[1], *K = ne[0]. GQ_ERR_TYPE for another
+ * *type (GQ_TYPE_Q4_0, _Q8_0, _Q4_K or _MXFP4), *M = ne[1], *K = ne[0]. GQ_ERR_TYPE for another
  * data type, GQ_ERR_SHAPE for a tensor with more than two non-unit dimensions or an index
  * out of range.
  */
