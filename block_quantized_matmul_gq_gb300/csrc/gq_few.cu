@@ -15,14 +15,18 @@
 // used here: its operands would have to pass through shared memory once more, with the
 // scales applied there, and its 128-row tiles leave most SMs without work at these sizes.
 //
-// Layout of the work. A unit is (a group of up to 16 tokens, a tile of 32 weight rows per
-// warp). The four warps of a CTA take four row tiles or split a tile's K range (kshift).
-// Every warp runs its own ring of bulk copies: one copy per weight row and chunk, starting at
-// the 16-byte word that holds the chunk's first byte, because rows of 17- and 18-byte blocks
-// start anywhere; the words are aligned in registers. The ring runs on across units, so the
-// next unit's weights are on their way while a unit ends. Weights do not depend on the kernel
-// before, so they start to stream before griddepcontrol.wait.
+// Layout of the work. One persistent CTA per SM, 16 warps, and a ring of stages, each some weight
+// rows x up to 64 blocks of K, one bulk copy per row: runs of about a kilobyte, which is what DRAM pages and the copy engine want (16-
+// byte cp.async in 136-byte runs reached 3.3 TB/s, bulk copies of 136 bytes 1.6). A row's copy
+// starts at the 16-byte word that holds its first byte, because rows of 17- and 18-byte blocks
+// start anywhere; words are aligned in registers. The warps split a stage's K range
+// (kwarps), four blocks of 32 rows each, so that the activations of those four blocks stay in
+// registers from stage to stage; then their sums join through shared memory in a fixed order, and the
+// barrier of that join frees the stage for its refill.
+// The ring runs on across units, and weights do not depend on the kernel before, so they start
+// to stream before griddepcontrol.wait.
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 
 #include "gq_few.cuh"
@@ -30,34 +34,32 @@
 namespace gq {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxBlocks = 4;              // of one warp and stage
 
 constexpr int64_t kFewMaxTokens = 4096;   // of one launch: bounds the workspace
 
 enum Mode { kDense = 0, kGateUp = 1, kDown = 2 };
 
 template <int T>
-struct Fmt;   // block bytes, 32-weight blocks per chunk, shared-memory pitch of a row's chunk
+struct Fmt;   // bytes of 32 weights, and the 16-row tiles that a consumer warp takes of a stage
 template <>
 struct Fmt<GQ_TYPE_Q4_0> {
-    static constexpr int bb = kQ4Bytes, cb = 8, pitch = 176;
+    static constexpr int bb = kQ4Bytes, tiles = 2;
 };
 template <>
 struct Fmt<GQ_TYPE_Q8_0> {
-    static constexpr int bb = kQ8Bytes, cb = 4, pitch = 176;
+    static constexpr int bb = kQ8Bytes, tiles = 1;   // twice the bytes: the same stage
 };
 template <>
-struct Fmt<GQ_TYPE_Q4_K> {   // bb: a super-block's bytes over its 8 sub-blocks
-    static constexpr int bb = kQ4KBytes / 8, cb = 8, pitch = 144;
+struct Fmt<GQ_TYPE_Q4_K> {   // a super-block's bytes over its 8 sub-blocks
+    static constexpr int bb = kQ4KBytes / 8, tiles = 2;
 };
 template <>
 struct Fmt<GQ_TYPE_MXFP4> {
-    static constexpr int bb = kMxfp4Bytes, cb = 8, pitch = 176;
+    static constexpr int bb = kMxfp4Bytes, tiles = 2;
 };
-// Pitches: a chunk is 136..144 bytes and starts up to 15 bytes into its first 16-byte word;
-// 176 = 44 words puts the eight rows that a warp reads at once on eight distinct groups of four
-// banks, as 144 = 36 words does where rows are always aligned (Q4_K).
 
 struct Params {
     const uint8_t* W;
@@ -66,30 +68,77 @@ struct Params {
     int64_t row_bytes;
     int rows;                 // weight rows (of one expert)
     int kb;                   // 32-weight blocks per row
-    int tiles;                // row tiles: ceil(rows / (32 row-warps))
-    int kshift;               // log2 of the warps that share a row tile by splitting K
+    int kc;                   // blocks of one stage (chunk) of a row
+    int chunks;               // ceil(kb / kc)
+    int kwarps;               // consumer warps that split a chunk, `per` blocks each
+    int per;
+    int units;                // of one group: row tiles of unit_rows
+    int pitch, stage_bytes;   // of a staged row, of a stage
+    int stages;
     const uint4* xb;          // split activations, 64 bytes per (row, term, block)
     const float* xm;          // their block factors: float2 (two terms) or float (one)
     int64_t N;                // tokens
     int E, top_k, pairs;
     const int* ids;
-    const float* weights;
-    float* Y;                 // kDense, kDown
+    float* Y;                 // kDense
     __half* hb;               // kGateUp: split activations of the result,
     float2* hm;
     int h_type;               //          in the order of the down matrices' type
     float* part;              // kDown: [pair][rows]
-    unsigned* arrived;        // kDown: per row tile
     unsigned* status;
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
+
+// c = A (16 weight rows x 16) . B (16 x 8 columns), then c += for the block's second half.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_next(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte i of w as fp32: 2^23 + byte under the exponent, less 2^23 (no conversion unit).
+__device__ __forceinline__ float byte_to_float(uint32_t w, int i) {
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, i ? 0x7651 : 0x7650)) - 8388608.0f;
+}
+
+// Two E8M0 scale bytes to fp32 (255: NaN; 0: the subnormal 2^-127).
+__device__ __forceinline__ void e8m0_to_f32(uint32_t lo, uint32_t hi, float& dlo, float& dhi) {
+    uint32_t r;
+    const unsigned short both = static_cast<unsigned short>(lo | (hi << 8));
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(both));
+    dlo = __uint_as_float(r << 16);
+    dhi = __uint_as_float(r & 0xFFFF0000u);
 }
 
 // fp16 arithmetic on pairs: 1024 + u lies in an fp16 word as 0x6400 | u, so integers become
@@ -134,49 +183,42 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 
-// Products of one 16-row tile with one block, for NT column tiles:
-// tot += d_row s_token (codes . columns).
-template <int MT, int NT, int Terms>
-struct Totals {
-    // [row tile][row g or g + 8][column tile][two terms: token t; one term: tokens 2t, 2t + 1]
-    float v[MT][2][NT][Terms == 2 ? 1 : 2];
-};
-
+// One block's activations in this lane.
 template <int NT, int Terms>
 struct Columns {
-    uint4 b[NT];        // this lane's eight fp16 of column g
-    float2 m[NT];       // {scale, sum} of token t (two terms), or x, y of tokens 2t, 2t + 1 (one)
+    uint4 b[NT];               // eight fp16 of column g
+    float2 m[NT];              // {scale, sum} of token t (two terms), scales of 2t, 2t + 1 (one)
 };
 
+// Products of one 16-row tile with one block, for NT column tiles: tot += d_row s_token (codes
+// . columns), less m_row sum_token for Q4_K. tot: [column tile][rows g, g + 8][tokens].
 template <int T, int Terms, int NT>
-__device__ __forceinline__ void block_products(const uint32_t (&lo)[4], const uint32_t (&hi)[4],
-                                               float dlo, float dhi, float mlo, float mhi,
-                                               const Columns<NT, Terms>& col,
-                                               float (&t0)[NT][Terms == 2 ? 1 : 2],
-                                               float (&t1)[NT][Terms == 2 ? 1 : 2]) {
+__device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const float (&d)[2],
+                                               const float (&m)[2], const Columns<NT, Terms>& col,
+                                               float (&tot)[NT][2][3 - Terms]) {
+    float c[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma16816(c, lo[0], hi[0], lo[1], hi[1], col.b[n].x, col.b[n].y);
-        mma16816(c, lo[2], hi[2], lo[3], hi[3], col.b[n].z, col.b[n].w);
-        if (Terms == 2) {
-            t0[n][0] = fmaf(dlo * col.m[n].x, c[0] + c[1], t0[n][0]);
-            t1[n][0] = fmaf(dhi * col.m[n].x, c[2] + c[3], t1[n][0]);
-            if (T == GQ_TYPE_Q4_K) {
-                t0[n][0] = fmaf(-mlo, col.m[n].y, t0[n][0]);
-                t1[n][0] = fmaf(-mhi, col.m[n].y, t1[n][0]);
+    for (int n = 0; n < NT; ++n)
+        mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n].x, col.b[n].y);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n].z, col.b[n].w);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (Terms == 2) {
+                tot[n][h][0] = fmaf(d[h] * col.m[n].x, c[n][2 * h] + c[n][2 * h + 1], tot[n][h][0]);
+                if constexpr (T == GQ_TYPE_Q4_K) tot[n][h][0] = fmaf(-m[h], col.m[n].y, tot[n][h][0]);
+            } else {
+                tot[n][h][0] = fmaf(d[h] * col.m[n].x, c[n][2 * h], tot[n][h][0]);
+                tot[n][h][1] = fmaf(d[h] * col.m[n].y, c[n][2 * h + 1], tot[n][h][1]);
             }
-        } else {
-            t0[n][0] = fmaf(dlo * col.m[n].x, c[0], t0[n][0]);
-            t0[n][Terms == 2 ? 0 : 1] = fmaf(dlo * col.m[n].y, c[1], t0[n][Terms == 2 ? 0 : 1]);
-            t1[n][0] = fmaf(dhi * col.m[n].x, c[2], t1[n][0]);
-            t1[n][Terms == 2 ? 0 : 1] = fmaf(dhi * col.m[n].y, c[3], t1[n][Terms == 2 ? 0 : 1]);
         }
-    }
 }
 
 // The shared lists of a launch over experts: pairs sorted by expert, and groups of up to
-// kFewGroup2 pairs of one expert.
+// kFewGroup pairs of one expert.
 struct Lists {
     uint16_t pair[kMoeMaxPairs];
     uint16_t expert[kMoeMaxPairs];
@@ -197,7 +239,6 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
         ids[q] = id >= 0 && id < p.E ? id : -1;
     }
     __syncthreads();
-    constexpr int kPer = kMoeMaxPairs / kThreads;
     if (threadIdx.x < 32) {
         const unsigned below = (1u << threadIdx.x) - 1u;
         for (int q0 = 0; q0 < p.pairs; q0 += 32) {
@@ -220,7 +261,7 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + threadIdx.x;
             const int c = e < p.E ? count[e] : 0;
-            const int g = (c + kFewGroup2 - 1) / kFewGroup2;
+            const int g = (c + kFewGroup - 1) / kFewGroup;
             int incl = c | (g << 16);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -231,8 +272,8 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
             const int pair0 = excl & 0xFFFF, group0 = excl >> 16;
             for (int i = 0; i < g; ++i) {
                 L.expert[group0 + i] = static_cast<uint16_t>(e);
-                L.start[group0 + i] = static_cast<uint16_t>(pair0 + i * kFewGroup2);
-                L.count[group0 + i] = static_cast<uint8_t>(min(kFewGroup2, c - i * kFewGroup2));
+                L.start[group0 + i] = static_cast<uint16_t>(pair0 + i * kFewGroup);
+                L.count[group0 + i] = static_cast<uint8_t>(min(kFewGroup, c - i * kFewGroup));
             }
             if (e < p.E) count[e] = pair0;
             base += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -240,516 +281,500 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
         if (threadIdx.x == 0) L.groups = base >> 16;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int q = threadIdx.x + i * kThreads;
-        if (q < p.pairs && ids[q] >= 0)
-            L.pair[count[ids[q] & 0xFFFF] + (ids[q] >> 16)] = static_cast<uint16_t>(q);
-    }
+    for (int q = threadIdx.x; q < p.pairs; q += kThreads)
+        if (ids[q] >= 0) L.pair[count[ids[q] & 0xFFFF] + (ids[q] >> 16)] = static_cast<uint16_t>(q);
     __syncthreads();
 }
 
-template <int T, int M, int Terms>
-struct Few {
-    static constexpr int kMT = M == kGateUp ? 4 : 2;          // 16-row tiles per warp
-    static constexpr int kRows = 16 * kMT;                    // weight rows per warp and chunk
-    static constexpr int kPitch = Fmt<T>::pitch;
-    static constexpr int kStageBytes = kRows * kPitch + 16;   // the last word's second half
-    static constexpr int kStages = M == kGateUp ? 2 : 4;
-    static constexpr int kGroup = Terms == 2 ? kFewGroup2 : kFewGroup1;
-    static constexpr int kTotals = kMT * 2 * 4 * (Terms == 2 ? 1 : 2);   // floats a lane, NT = 4
-    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-    static constexpr int kSumBytes = (kWarps - 1) * kTotals * 32 * 4;
-    static constexpr int kSmem = kRingBytes + kSumBytes + static_cast<int>(sizeof(Lists)) + 16;
-    static_assert((kMoeMaxExperts + kMoeMaxPairs) * 4 <= kRingBytes, "the lists' scratch lies in the ring");
+// One warp writes a block of a split activation row: lane i holds element i. `xb` and `xm` are
+// the row's places of this block; `lo_at` the distance from hi to lo.
+__device__ __forceinline__ void write_split(float x, int lane, int place, __half* xb, int64_t lo_at,
+                                            float2* xm) {
+    const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
+    const int e = block_exponent(amax);
+    const float xs = x * pow2f(14 - e);
+    const __half hi = __float2half_rn(xs);
+    const __half lo = __float2half_rn(xs - __half2float(hi));
+    float sum = __half2float(hi) + __half2float(lo);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    xb[place] = hi;
+    xb[lo_at + place] = lo;
+    if (lane == 0) {
+        const float s = pow2f(e - 14);
+        *xm = make_float2(s, s * sum);
+    }
+}
+
+// Shared memory: the lists (and, of kGateUp, the hidden values of a unit), the consumers' sums,
+// the ring.
+constexpr int kSumFloats = 2 * kWarps * 32 * (kFewGroup + 1);   // two halves, in turn
+constexpr int kHiddenFloats = 64 * (kFewGroup + 1);
+constexpr int kListBytes = (static_cast<int>(sizeof(Lists)) + 127) / 128 * 128;
+constexpr int kRingAt = kListBytes + (kSumFloats + kHiddenFloats) * 4;
+constexpr int kMaxStages = 5;
+constexpr int kSmemMax = 227 * 1024 - 512;   // 512: the barriers and what else is static
+static_assert(kRingAt % 128 == 0 && (kMoeMaxExperts + kMoeMaxPairs) * 4 <= kSumFloats * 4,
+              "the lists' scratch lies in the sums");
+
+// A unit: group, row tile, and how many this CTA has from here on.
+struct Place {
+    int gi, tile;
+    int64_t left;
+    __device__ __forceinline__ void next(int units) {
+        --left;
+        if (++tile == units) {
+            tile = 0;
+            ++gi;
+        }
+    }
 };
 
 template <int T, int M, int Terms>
 struct Worker {
-    using F = Few<T, M, Terms>;
+    static constexpr int kTiles = Fmt<T>::tiles;
+    static constexpr int kBB = Fmt<T>::bb;
     const Params& p;
     const Lists& L;
-    uint8_t* ring;      // this warp's
-    float* sums;        // the CTA's
-    uint64_t* bars;     // this warp's, kStages
-    int lane, wk, wr, kwarps, rwarps, chunks;
-    int units;
-    // copies: next (unit, chunk) to issue and its stage; consumption: stage and phase
-    int iu, ic, istage;
-    int irow0;
-    int64_t ie_row;
-    int cstage;
-    uint32_t cphase;
+    float* sums;
+    float* hidden;
+    uint32_t ring, full;          // shared addresses
+    int lane, warp;
+    int stage_rows;               // staged rows
+    int sub;                      // stages of a unit and chunk (kGateUp: a unit is whole 32-blocks)
+    int res_shift;                // log2 of a stage's result rows
+    int groups;
+    Place f;                      // the next stage to fill: unit,
+    int fs, fc, fslot;            // stage in it, chunk; slot
     bool dead;
 
-    __device__ __forceinline__ int group_of(int unit) const { return unit / p.tiles; }
     __device__ __forceinline__ int expert_of(int gi) const { return M == kDense ? 0 : L.expert[gi]; }
     __device__ __forceinline__ int count_of(int gi) const {
         if (M != kDense) return L.count[gi];
-        return static_cast<int>(min(static_cast<int64_t>(F::kGroup),
-                                    p.N - static_cast<int64_t>(gi) * F::kGroup));
+        return static_cast<int>(min(static_cast<int64_t>(kFewGroup),
+                                    p.N - static_cast<int64_t>(gi) * kFewGroup));
     }
     // activation row of column token i of a group
     __device__ __forceinline__ int64_t x_row(int gi, int i) const {
-        if (M == kDense) return static_cast<int64_t>(gi) * F::kGroup + i;
+        if (M == kDense) return static_cast<int64_t>(gi) * kFewGroup + i;
         const int q = L.pair[L.start[gi] + i];
         return M == kGateUp ? q / p.top_k : q;
     }
-    __device__ __forceinline__ int first_row(int unit) const {
-        return ((unit % p.tiles) * rwarps + wr) * 32;
+    // Result rows of a stage; a kGateUp tile is 8 gate rows and the 8 up rows of the same numbers.
+    __device__ __forceinline__ int first_row(int tile, int s) const { return (tile * sub + s) << res_shift; }
+    __device__ __forceinline__ static int row_in_stage(int sr) {
+        return M == kGateUp ? (sr >> 4) * 8 + (sr & 7) : sr;
     }
 
-    __device__ __forceinline__ void issue_from(int unit) {
-        iu = unit;
-        ic = wk;
-        if (iu >= units) return;
-        irow0 = first_row(iu);
-        ie_row = static_cast<int64_t>(expert_of(group_of(iu))) * p.rows;
-    }
+    // ---- copies ----
 
-    // Starts the copies of the next chunk (if any) into the next stage.
-    __device__ __forceinline__ void issue() {
-        if (iu >= units) return;
-        const int r = irow0 + lane;
-        const int nb = min(Fmt<T>::cb, p.kb - ic * Fmt<T>::cb);
-        const uint32_t bar = smem_addr(&bars[istage]);
-        uint8_t* dst = ring + istage * F::kStageBytes + lane * F::kPitch;
-        uint32_t bytes = 0;
-        int64_t from = 0;
-        if (r < p.rows) {
-            const int64_t start = (ie_row + r) * p.row_bytes + static_cast<int64_t>(ic) * (Fmt<T>::cb * Fmt<T>::bb);
-            from = start & ~static_cast<int64_t>(15);
-            int64_t to = (start + nb * Fmt<T>::bb + 15) & ~static_cast<int64_t>(15);
-            if (to > p.total_bytes) {   // the matrix ends inside its last 16-byte word
-                to = p.total_bytes & ~static_cast<int64_t>(15);
-                for (int64_t i = to > from ? to : from; i < p.total_bytes; ++i) {
-                    dst[i - from] = p.W[i];
-                    if (M == kGateUp) dst[32 * F::kPitch + (i - from)] = p.W2[i];
+    // Starts the copies of the next stage, if there is one: warp w copies rows w, w + 16, ... of
+    // up to 128, a lane each. Every row arrives once on the stage's barrier.
+    __device__ __forceinline__ void fill() {
+        if (f.left == 0) return;
+        const int sr = warp + kWarps * lane;
+        if (sr < stage_rows) {
+            const uint32_t dst = ring + fslot * p.stage_bytes + sr * p.pitch;
+            const uint32_t bar = full + 8 * fslot;
+            const int r = ((f.tile * sub + fs) << res_shift) + row_in_stage(sr);
+            const uint8_t* W = M == kGateUp && (sr & 8) ? p.W2 : p.W;
+            uint32_t n = 0;
+            int64_t from = 0;
+            if (r < p.rows) {
+                const int64_t row = static_cast<int64_t>(expert_of(f.gi)) * p.rows + r;
+                const int64_t start = row * p.row_bytes + fc * p.kc * kBB;
+                from = start & ~static_cast<int64_t>(15);
+                int64_t to = (start + min(p.kc, p.kb - fc * p.kc) * kBB + 15) & ~static_cast<int64_t>(15);
+                if (to > p.total_bytes) {   // the matrix ends inside its last 16-byte word
+                    to = p.total_bytes & ~static_cast<int64_t>(15);
+                    for (int64_t k = to > from ? to : from; k < p.total_bytes; ++k)
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(k - from)),
+                                     "r"(static_cast<uint32_t>(W[k])) : "memory");
                 }
+                if (to > from) n = static_cast<uint32_t>(to - from);
             }
-            bytes = to > from ? static_cast<uint32_t>(to - from) : 0u;
+            // the stage's plain reads, before the barrier that brought us here, come first
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive_expect_tx(bar, n);
+            if (n > 0) bulk_g2s_evict_first(dst, W + from, n, bar);
         }
-        mbar_arrive_expect_tx(bar, M == kGateUp ? 2 * bytes : bytes);
-        if (bytes > 0) {
-            bulk_g2s_evict_first(smem_addr(dst), p.W + from, bytes, bar);
-            if (M == kGateUp)
-                bulk_g2s_evict_first(smem_addr(dst) + 32 * F::kPitch, p.W2 + from, bytes, bar);
+        if (++fslot == p.stages) fslot = 0;
+        if (++fc == p.chunks) {
+            fc = 0;
+            if (++fs == sub) {
+                fs = 0;
+                f.next(p.units);
+            }
         }
-        istage = istage + 1 == F::kStages ? 0 : istage + 1;
-        ic += kwarps;
-        if (ic >= chunks) issue_from(iu + gridDim.x);
     }
 
-    // Waits for the copies of the stage at hand; after a wait that ran out, for those of the
-    // others too (again with a limit), so that none is in flight when the CTA leaves.
-    __device__ __forceinline__ void wait_stage() {
-        if (dead) return;
-        const bool ok = mbar_wait(smem_addr(&bars[cstage]), cphase);
-        if (__all_sync(0xFFFFFFFFu, ok)) return;
+    // Waits for the stage at hand. After a wait that ran out, and an equal one for the other
+    // stages that are under way, goes on without waiting: the results are lost.
+    __device__ __forceinline__ void wait_stage(int slot, uint32_t phase) {
+        if (dead || __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * slot, phase))) return;
         dead = true;
         report_status(p.status, kStatusTimeout);
-        for (int i = 1, st = cstage, ph = cphase; i < F::kStages; ++i) {
-            if (++st == F::kStages) {
-                st = 0;
-                ph ^= 1;
+        for (int i = 1; i < p.stages; ++i) {
+            if (++slot == p.stages) {
+                slot = 0;
+                phase ^= 1;
             }
-            mbar_wait(smem_addr(&bars[st]), ph);
+            mbar_wait(full + 8 * slot, phase);
         }
     }
 
+    // ---- products ----
+
     template <int NT>
-    __device__ __forceinline__ void load_columns(Columns<NT, Terms>& col, const uint4* const (&xp)[NT],
-                                                 const float* const (&mp)[NT][Terms == 2 ? 1 : 2],
-                                                 int kb) const {
+    struct Acts {
+        Columns<NT, Terms> col[kMaxBlocks];
+    };
+
+    // This lane's share of nb blocks from block kb0 of the group's activations. Columns of
+    // tokens that the group does not have read token 0's: nothing uses them.
+    template <int NT>
+    __device__ __forceinline__ void load_acts(Acts<NT>& a, int gi, int n_tok, int kb0, int nb) const {
+        const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            col.b[n] = xp[n] ? xp[n][static_cast<int64_t>(kb) * 4] : make_uint4(0u, 0u, 0u, 0u);
-            if (Terms == 2) {
-                col.m[n] = mp[n][0] ? reinterpret_cast<const float2*>(mp[n][0])[kb]
-                                    : make_float2(0.0f, 0.0f);
+            const int i = Terms == 2 ? 4 * n + (g >> 1) : 8 * n + g;
+            const int64_t row = x_row(gi, i < n_tok ? i : 0) * Terms + (Terms == 2 ? g & 1 : 0);
+            const uint4* xp = p.xb + (row * p.kb + kb0) * 4 + t;
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b)
+                if (b < nb) a.col[b].b[n] = xp[b * 4];
+            if constexpr (Terms == 2) {
+                const int j = 4 * n + t;
+                const float2* mp = reinterpret_cast<const float2*>(p.xm) + x_row(gi, j < n_tok ? j : 0) * p.kb + kb0;
+#pragma unroll
+                for (int b = 0; b < kMaxBlocks; ++b)
+                    if (b < nb) a.col[b].m[n] = mp[b];
             } else {
-                col.m[n].x = mp[n][0] ? mp[n][0][kb] : 0.0f;
-                col.m[n].y = mp[n][Terms == 2 ? 0 : 1] ? mp[n][Terms == 2 ? 0 : 1][kb] : 0.0f;
+                const int j0 = 8 * n + 2 * t;
+                const float* m0 = p.xm + x_row(gi, j0 < n_tok ? j0 : 0) * p.kb + kb0;
+                const float* m1 = p.xm + x_row(gi, j0 + 1 < n_tok ? j0 + 1 : 0) * p.kb + kb0;
+#pragma unroll
+                for (int b = 0; b < kMaxBlocks; ++b)
+                    if (b < nb) a.col[b].m[n] = make_float2(m0[b], m1[b]);
             }
         }
     }
 
-    // One chunk (nb blocks from block kb0) out of the stage's shared memory.
+    // nb blocks, from block kb0 of the row (kq0 of the chunk), of this warp's rows of a stage.
     template <int NT>
-    __device__ __forceinline__ void chunk(Totals<F::kMT, NT, Terms>& tot, Columns<NT, Terms>& col,
-                                          const uint4* const (&xp)[NT],
-                                          const float* const (&mp)[NT][Terms == 2 ? 1 : 2],
-                                          const uint8_t* stage, int64_t e_row, int row0, int c,
-                                          int next_kb) {
-        constexpr int kCB = Fmt<T>::cb, kBB = Fmt<T>::bb;
+    __device__ __forceinline__ void products(float (&tot)[kTiles][NT][2][3 - Terms], const Acts<NT>& a,
+                                             uint32_t stage, uint32_t row0, int c, int kq0, int nb) const {
         const int g = lane >> 2, t = lane & 3;
-        const int kb0 = c * kCB;
-        const int nb = min(kCB, p.kb - kb0);
-        // Where this lane's rows begin inside their staged words (0..15). Rows g and g + 8 of
-        // every tile agree in the low two bits, since eight rows are a multiple of 8 bytes.
-        const uint8_t* base[F::kMT][2];
+        const int wr = warp / p.kwarps;
+        // Where this lane's rows begin: the staged word's offset (0..15) of their chunk. Rows g
+        // and g + 8 of every tile agree in the low two bits, as eight rows are a multiple of 8
+        // bytes.
+        uint32_t base[kTiles][2];
 #pragma unroll
-        for (int mt = 0; mt < F::kMT; ++mt)
+        for (int ti = 0; ti < kTiles; ++ti)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int rr = 16 * mt + 8 * h + g;
-                const uint32_t row = static_cast<uint32_t>(e_row) + static_cast<uint32_t>(row0 + (rr & 31));
-                const uint32_t mis = (row * static_cast<uint32_t>(p.row_bytes) +
-                                      static_cast<uint32_t>(c) * (kCB * kBB)) & 15u;
-                base[mt][h] = stage + rr * F::kPitch + mis;
+                const int sr = (wr * kTiles + ti) * 16 + 8 * h + g;
+                const uint32_t mis = ((row0 + row_in_stage(sr)) * static_cast<uint32_t>(p.row_bytes) +
+                                      static_cast<uint32_t>(c * p.kc) * kBB) & 15u;
+                base[ti][h] = stage + sr * p.pitch + mis;
             }
-        const uint32_t r3 = smem_addr(base[0][0]) & 3u;
         if constexpr (T == GQ_TYPE_Q4_K) {
-            uint4 hd[F::kMT][2];
+            // four (or two) sub-blocks of one super-block
+            const int in = (kq0 & 7) >> 1;
 #pragma unroll
-            for (int mt = 0; mt < F::kMT; ++mt)
+            for (int ti = 0; ti < kTiles; ++ti) {
+                uint4 hd[2];
+                float D[2], Dm[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) hd[mt][h] = *reinterpret_cast<const uint4*>(base[mt][h]);
+                for (int h = 0; h < 2; ++h) {
+                    base[ti][h] += (kq0 >> 3) * kQ4KBytes;
+                    hd[h] = lds128(base[ti][h]);
+                    base[ti][h] += 16 + 32 * in + 4 * t;
+                    D[h] = half_bits_to_float(hd[h].x);
+                    Dm[h] = half_bits_to_float(hd[h].x >> 16);
+                }
 #pragma unroll
-            for (int b = 0; b < 8; b += 2) {
-                uint32_t w[F::kMT][2][2];
-#pragma unroll
-                for (int mt = 0; mt < F::kMT; ++mt)
+                for (int b = 0; b < kMaxBlocks; b += 2) {
+                    if (b >= nb) break;
+                    uint32_t w[2][2], sc[2], mn[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint8_t* a = base[mt][h] + 16 + 16 * b + 4 * t;
-                        w[mt][h][0] = *reinterpret_cast<const uint32_t*>(a);
-                        w[mt][h][1] = *reinterpret_cast<const uint32_t*>(a + 16);
+                        w[h][0] = lds32(base[ti][h] + 16 * b);
+                        w[h][1] = lds32(base[ti][h] + 16 + 16 * b);
+                        q4k_scales(hd[h], in + (b >> 1), sc[h], mn[h]);
                     }
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    Columns<NT, Terms> cur = col;
-                    if (b + s + 1 < 8)
-                        load_columns<NT>(col, xp, mp, kb0 + b + s + 1);
-                    else if (next_kb >= 0)
-                        load_columns<NT>(col, xp, mp, next_kb);
-#pragma unroll
-                    for (int mt = 0; mt < F::kMT; ++mt) {
+                    for (int s = 0; s < 2; ++s) {
                         uint32_t q[2][4];
                         float d[2], m[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t mask = s ? 0x00F000F0u : 0x000F000Fu;
-                            const uint32_t w0 = w[mt][h][0], w1 = w[mt][h][1];
-                            q[h][0] = (w0 & mask) | kMagic;
-                            q[h][1] = ((w0 >> 8) & mask) | kMagic;
-                            q[h][2] = (w1 & mask) | kMagic;
-                            q[h][3] = ((w1 >> 8) & mask) | kMagic;
+                            q[h][0] = (w[h][0] & mask) | kMagic;
+                            q[h][1] = ((w[h][0] >> 8) & mask) | kMagic;
+                            q[h][2] = (w[h][1] & mask) | kMagic;
+                            q[h][3] = ((w[h][1] >> 8) & mask) | kMagic;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 q[h][i] = s ? h2_fma(q[h][i], kSixteenth, 0xD400D400u)
                                             : h2_sub(q[h][i], kMagic);
-                            uint32_t sc, mn;
-                            q4k_scales(hd[mt][h], b >> 1, sc, mn);
-                            d[h] = half_bits_to_float(hd[mt][h].x) * static_cast<float>((sc >> (8 * s)) & 0xFFu);
-                            m[h] = half_bits_to_float(hd[mt][h].x >> 16) *
-                                   static_cast<float>((mn >> (8 * s)) & 0xFFu);
+                            d[h] = D[h] * byte_to_float(sc[h], s);
+                            m[h] = Dm[h] * byte_to_float(mn[h], s);
                         }
-                        block_products<T, Terms, NT>(q[0], q[1], d[0], d[1], m[0], m[1], cur,
-                                                     tot.v[mt][0], tot.v[mt][1]);
+                        block_products<T, Terms, NT>(q, d, m, a.col[b + s], tot[ti]);
                     }
                 }
             }
-            return;
-        }
-        // Unaligned words: the aligned word at (base + delta[j] + 4-multiple) and its
-        // successor, shifted by shift[j], for byte offsets congruent j modulo 4.
-        int delta[4];
-        uint32_t shift[4];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            delta[j] = (r3 + j >= 4 ? 4 : 0) - static_cast<int>(r3) + 4 * t;
-            shift[j] = (r3 + j) << 3;   // the funnel shift takes it modulo 32
-        }
+            for (int ti = 0; ti < kTiles; ++ti)
 #pragma unroll
-        for (int b = 0; b < kCB; ++b) {
-            if (b < nb) {
-                Columns<NT, Terms> cur = col;
-                if (b + 1 < nb)
-                    load_columns<NT>(col, xp, mp, kb0 + b + 1);
-                else if (next_kb >= 0)
-                    load_columns<NT>(col, xp, mp, next_kb);
+                for (int h = 0; h < 2; ++h) base[ti][h] += kq0 * kBB;
+            // Unaligned words: the aligned word at (base + delta[j] + 4-multiple) and its
+            // successor, shifted by shift[j], for byte offsets congruent j modulo 4.
+            const uint32_t r3 = base[0][0] & 3u;
+            int delta[4];
+            uint32_t shift[4];
 #pragma unroll
-                for (int mt = 0; mt < F::kMT; ++mt) {
+            for (int j = 0; j < 4; ++j) {
+                delta[j] = (r3 + j >= 4 ? 4 : 0) - static_cast<int>(r3) + 4 * t;
+                shift[j] = (r3 + j) << 3;   // the funnel shift takes it modulo 32
+            }
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) {
+                if (b >= nb) break;
+#pragma unroll
+                for (int ti = 0; ti < kTiles; ++ti) {
                     uint32_t q[2][4];
-                    float d[2];
+                    float d[2], m[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         constexpr int kHead = T == GQ_TYPE_MXFP4 ? 1 : 2;
                         const int off = b * kBB + kHead;
-                        const uint8_t* a = base[mt][h] + delta[off & 3];
-                        const uint32_t* w = reinterpret_cast<const uint32_t*>(a + (off & ~3));
-                        const uint32_t w0 = __funnelshift_r(w[0], w[1], shift[off & 3]);
-                        if (T == GQ_TYPE_Q8_0) {
-                            const uint32_t w1 = __funnelshift_r(w[4], w[5], shift[off & 3]);
+                        const uint32_t at = base[ti][h] + delta[off & 3] + (off & ~3);
+                        const uint32_t w0 = __funnelshift_r(lds32(at), lds32(at + 4), shift[off & 3]);
+                        if constexpr (T == GQ_TYPE_Q8_0) {
+                            const uint32_t w1 = __funnelshift_r(lds32(at + 16), lds32(at + 20), shift[off & 3]);
                             const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
                             // 1024 + 128 + code, byte by byte under the exponent
                             q[h][0] = h2_sub(__byte_perm(u0, 0x64u, 0x4140), 0x64806480u);
                             q[h][1] = h2_sub(__byte_perm(u0, 0x64u, 0x4342), 0x64806480u);
                             q[h][2] = h2_sub(__byte_perm(u1, 0x64u, 0x4140), 0x64806480u);
                             q[h][3] = h2_sub(__byte_perm(u1, 0x64u, 0x4342), 0x64806480u);
-                        } else if (T == GQ_TYPE_Q4_0) {
+                        } else if constexpr (T == GQ_TYPE_Q4_0) {
                             nibbles_to_f16<8>(w0, q[h]);
                         } else {
                             e2m1_to_f16(w0, q[h]);
                         }
-                        d[h] = T == GQ_TYPE_MXFP4
-                                   ? mx_scale(base[mt][h][b * kBB])
-                                   : half_bits_to_float(*reinterpret_cast<const unsigned short*>(
-                                         base[mt][h] + b * kBB));
+                        if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(lds16(base[ti][h] + b * kBB));
                     }
-                    block_products<T, Terms, NT>(q[0], q[1], d[0], d[1], 0.0f, 0.0f, cur,
-                                                 tot.v[mt][0], tot.v[mt][1]);
+                    if constexpr (T == GQ_TYPE_MXFP4)
+                        e8m0_to_f32(lds8(base[ti][0] + b * kBB), lds8(base[ti][1] + b * kBB), d[0], d[1]);
+                    block_products<T, Terms, NT>(q, d, m, a.col[b], tot[ti]);
                 }
             }
         }
     }
 
-    // Adds the K ranges' totals in warp order into the wk == 0 warps.
+    // The units of this CTA from `at` on whose groups have as many tokens as NT column tiles are
+    // for.
     template <int NT>
-    __device__ __forceinline__ void join(Totals<F::kMT, NT, Terms>& tot) {
-        if (kwarps == 1) return;
-        constexpr int kN = F::kMT * 2 * NT * (Terms == 2 ? 1 : 2);
-        float* mine = &tot.v[0][0][0][0];
-        if (wk > 0) {
-            float* to = sums + (wr * (kwarps - 1) + wk - 1) * F::kTotals * 32 + lane;
+    __device__ __forceinline__ void consume(Place& at, int& slot, uint32_t& phase) {
+        constexpr int kTile = 4 * (3 - Terms);
+        constexpr int kPitch = NT * kTile + 1;   // of a row of sums
+        const int wk = warp & (p.kwarps - 1);
+        const int kq0 = wk * p.per;
+        Acts<NT> acts;
+        int held = -1, side = 0;
+        __syncthreads();   // the sums are free
+#pragma unroll 1
+        for (; at.left > 0; at.next(p.units)) {
+            const int n_tok = count_of(at.gi);
+            if (n_tok > NT * kTile || n_tok <= (NT - 1) * kTile) break;
+            const uint32_t e_row = static_cast<uint32_t>(expert_of(at.gi)) * static_cast<uint32_t>(p.rows);
+#pragma unroll 1
+            for (int s = 0; s < sub; ++s) {
+                float tot[kTiles][NT][2][3 - Terms];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) to[i * 32] = mine[i];
-        }
-        __syncthreads();
-        if (wk == 0) {
-            for (int k = 0; k < kwarps - 1; ++k) {
-                const float* from = sums + (wr * (kwarps - 1) + k) * F::kTotals * 32 + lane;
+                for (int i = 0; i < kTiles * NT * 2 * (3 - Terms); ++i) (&tot[0][0][0][0])[i] = 0.0f;
+                const int row0 = first_row(at.tile, s);
+#pragma unroll 1
+                for (int c = 0; c < p.chunks; ++c) {
+                    const int nb = min(p.per, min(p.kc, p.kb - c * p.kc) - kq0);
+                    if (held != at.gi || p.chunks > 1) {
+                        load_acts<NT>(acts, at.gi, n_tok, c * p.kc + kq0, nb);
+                        held = at.gi;
+                    }
+                    wait_stage(slot, phase);
+                    if (nb > 0) products<NT>(tot, acts, ring + slot * p.stage_bytes, e_row + row0, c, kq0, nb);
+                    if (++slot == p.stages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    if (c + 1 < p.chunks) {   // after the last chunk, the join's barrier does this
+                        __syncthreads();
+                        if (!dead) fill();
+                    }
+                }
+                // Two halves of the sums in turn: one barrier is enough.
+                float* const half = sums + (side ? kSumFloats / 2 : 0);
+                side ^= 1;
+                float* mine = half + (warp * kTiles * 16 + (lane >> 2)) * kPitch;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) mine[i] += from[i * 32];
+                for (int ti = 0; ti < kTiles; ++ti)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 3 - Terms; ++i) {
+                                const int tok = Terms == 2 ? 4 * n + (lane & 3) : 8 * n + 2 * (lane & 3) + i;
+                                mine[(16 * ti + 8 * h) * kPitch + tok] = tot[ti][n][h][i];
+                            }
+                __syncthreads();
+                if (!dead) fill();
+                finish<kPitch>(half, at.gi, n_tok, s, row0);
             }
+            if constexpr (M == kGateUp) split_hidden(at.gi, n_tok, at.tile);
         }
-        __syncthreads();
     }
 
-    template <int NT>
-    __device__ __forceinline__ void unit(int u) {
-        const int gi = group_of(u), n_tok = count_of(gi);
-        const int64_t e_row = static_cast<int64_t>(expert_of(gi)) * p.rows;
-        const int row0 = first_row(u);
-        const int g = lane >> 2, t = lane & 3;
-        const uint4* xp[NT];
-        const float* mp[NT][Terms == 2 ? 1 : 2];
+    // Staged row sr, token i: the K warps' sums in their order.
+    template <int Pitch>
+    __device__ __forceinline__ float joined(const float* at, int sr, int i) const {
+        constexpr int kRows = 16 * kTiles;
+        const float* from = at + ((sr / kRows) * p.kwarps * kRows + sr % kRows) * Pitch + i;
+        float v = 0.0f;
+        for (int k = 0; k < p.kwarps; k += 4) {   // 4, 8 or 16 of them
+            float x[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int i = Terms == 2 ? 4 * n + (g >> 1) : 8 * n + g;
-            xp[n] = nullptr;
-            if (i < n_tok)
-                xp[n] = p.xb + ((x_row(gi, i) * Terms + (Terms == 2 ? g & 1 : 0)) * p.kb) * 4 + t;
+            for (int j = 0; j < 4; ++j) x[j] = from[(k + j) * kRows * Pitch];
 #pragma unroll
-            for (int s = 0; s < (Terms == 2 ? 1 : 2); ++s) {
-                const int j = Terms == 2 ? 4 * n + t : 8 * n + 2 * t + s;
-                mp[n][s] = nullptr;
-                if (j < n_tok) mp[n][s] = p.xm + x_row(gi, j) * p.kb * Terms;
-            }
+            for (int j = 0; j < 4; ++j) v += x[j];
         }
-        Totals<F::kMT, NT, Terms> tot;
-#pragma unroll
-        for (int i = 0; i < F::kMT * 2 * NT * (Terms == 2 ? 1 : 2); ++i) (&tot.v[0][0][0][0])[i] = 0.0f;
-        Columns<NT, Terms> col;
-        load_columns<NT>(col, xp, mp, wk * Fmt<T>::cb);
-        for (int c = wk; c < chunks; c += kwarps) {
-            wait_stage();
-            chunk<NT>(tot, col, xp, mp, ring + cstage * F::kStageBytes, e_row, row0, c,
-                      c + kwarps < chunks ? (c + kwarps) * Fmt<T>::cb : -1);
-            release_warp_to_async_proxy(__float_as_uint(tot.v[0][0][0][0]));
-            __syncwarp();
-            if (!dead) issue();
-            if (++cstage == F::kStages) {
-                cstage = 0;
-                cphase ^= 1;
-            }
-        }
-        join<NT>(tot);
-        if (wk == 0) finish<NT>(tot, gi, n_tok, row0);
-        if constexpr (M == kDown) arrive(u);
+        return v;
     }
 
-    template <int NT>
-    __device__ __forceinline__ void finish(Totals<F::kMT, NT, Terms>& tot, int gi, int n_tok, int row0) {
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+    template <int Pitch>
+    __device__ __forceinline__ void finish(const float* at, int gi, int n_tok, int s, int row0) const {
+        for (int i = threadIdx.x; i < (n_tok << res_shift); i += kThreads) {
+            const int r = i & ((1 << res_shift) - 1), tok = i >> res_shift;
             if constexpr (M == kGateUp) {
-                // rows 0-31 are gate, 32-63 up: this lane has elements g, 8 + g, 16 + g, 24 + g
-                // of the block and token t of both
-                float h[4];
-                uint32_t amax = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float gate = tot.v[i >> 1][i & 1][n][0];
-                    const float up = tot.v[(F::kMT / 2) + (i >> 1)][i & 1][n][0];
-                    h[i] = gate / (1.0f + expf(-gate)) * up;
-                    amax = max(amax, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-                }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                const int e = block_exponent(amax);
-                const float inv = pow2f(14 - e);
-                __half hi[4], lo[4];
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = h[i] * inv;
-                    hi[i] = __float2half_rn(x);
-                    lo[i] = __float2half_rn(x - __half2float(hi[i]));
-                    sum += __half2float(hi[i]) + __half2float(lo[i]);
-                }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                const int i_tok = 4 * n + t;
-                if (i_tok < n_tok && row0 < p.rows) {
-                    const int64_t q = L.pair[L.start[gi] + i_tok];
-                    const int64_t hb = p.rows / 32, blk = row0 / 32;
-                    __half* out = p.hb + (q * 2 * hb + blk) * 32;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = few_place(p.h_type, 8 * i + g);
-                        out[at] = hi[i];
-                        out[hb * 32 + at] = lo[i];
-                    }
-                    if (g == 0) {
-                        const float s = pow2f(e - 14);
-                        p.hm[q * hb + blk] =
-                            make_float2(s, s * sum);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < (Terms == 2 ? 1 : 2); ++s) {
-                    const int i_tok = Terms == 2 ? 4 * n + t : 8 * n + 2 * t + s;
-                    if (i_tok >= n_tok) break;
-                    float* out = M == kDown ? p.part : p.Y;
-                    out += x_row(gi, i_tok) * p.rows;
-#pragma unroll
-                    for (int mt = 0; mt < F::kMT; ++mt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int row = row0 + 16 * mt + 8 * h + g;
-                            if (row < p.rows) out[row] = tot.v[mt][h][n][s];
-                        }
-                }
+                const int sr = (r >> 3) * 16 + (r & 7);
+                const float gate = joined<Pitch>(at, sr, tok), up = joined<Pitch>(at, sr + 8, tok);
+                hidden[((s << res_shift) + r) * (kFewGroup + 1) + tok] = gate / (1.0f + expf(-gate)) * up;
+            } else if (row0 + r < p.rows) {
+                float* const out = M == kDown ? p.part : p.Y;
+                out[x_row(gi, tok) * p.rows + row0 + r] = joined<Pitch>(at, r, tok);
             }
         }
     }
 
-    // kDown: the CTA that ends a row tile last adds the pairs of every token, in the order of
-    // top_k, so the sum does not depend on which CTA that is.
-    __device__ __forceinline__ void arrive(int u) {
-        __shared__ bool last;
-        const int tile = u % p.tiles;
+    // kGateUp: the unit's hidden values to split activations, one warp per (block, token).
+    __device__ __forceinline__ void split_hidden(int gi, int n_tok, int tile) const {
         __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();
-            last = atomicAdd(&p.arrived[tile], 1u) + 1u == static_cast<unsigned>(L.groups);
-        }
-        __syncthreads();
-        if (last) {
-            __threadfence();
-            combine(tile);
-        }
-        __syncthreads();
-    }
-
-    __device__ __forceinline__ void combine(int tile) {
-        const int width = rwarps * 32, first = tile * width;
-        const int n_row = min(width, p.rows - first);
-        for (int i = threadIdx.x; i < static_cast<int>(p.N) * width; i += kThreads) {
-            const int n = i / width, r = i % width;
-            if (r >= n_row) continue;
-            float y = 0.0f;
-            for (int j = 0; j < p.top_k; ++j) {
-                const int q = n * p.top_k + j, id = p.ids[q];
-                if (id >= 0 && id < p.E)
-                    y = fmaf(p.weights[q], __ldcg(p.part + static_cast<int64_t>(q) * p.rows + first + r), y);
-            }
-            p.Y[static_cast<int64_t>(n) * p.rows + first + r] = y;
+        const int blocks = (sub << res_shift) / 32;   // 1 or 2
+        const int hb = p.rows / 32;
+        const int place = few_place(p.h_type, lane);
+        for (int i = warp; i < blocks * n_tok; i += kWarps) {
+            const int bl = i & (blocks - 1), tok = i / blocks;
+            const int blk = tile * blocks + bl;
+            if (blk >= hb) continue;
+            const int64_t q = L.pair[L.start[gi] + tok];
+            write_split(hidden[(32 * bl + lane) * (kFewGroup + 1) + tok], lane, place,
+                        p.hb + (q * 2 * hb + blk) * 32, hb * 32, p.hm + q * hb + blk);
         }
     }
 };
 
 template <int T, int M, int Terms>
-__global__ void __launch_bounds__(kThreads, 2) few_kernel(const Params p) {
-    using F = Few<T, M, Terms>;
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[kWarps * F::kStages];
-    Lists& L = *reinterpret_cast<Lists*>(smem + F::kRingBytes + F::kSumBytes);
+    __shared__ uint64_t bars[kMaxStages];
+    Lists& L = *reinterpret_cast<Lists*>(smem);
+    float* const sums = reinterpret_cast<float*>(smem + kListBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
-    if (threadIdx.x < kWarps * F::kStages) mbar_init(smem_addr(&bars[threadIdx.x]), 32);
+    Worker<T, M, Terms> w{p, L, sums, sums + kSumFloats, smem_addr(smem) + kRingAt, smem_addr(bars), lane, warp};
+    w.stage_rows = 16 * Fmt<T>::tiles * (kWarps / p.kwarps);
+    if (threadIdx.x < p.stages) mbar_init(smem_addr(&bars[threadIdx.x]), w.stage_rows);
     if (threadIdx.x == 0) fence_mbar_init();
+    if (M != kDense) build_lists(p, L, reinterpret_cast<int*>(sums));
     __syncthreads();
-    if (M != kDense) build_lists(p, L, reinterpret_cast<int*>(smem));
-    Worker<T, M, Terms> w{p, L, smem + warp * F::kStages * F::kStageBytes,
-                          reinterpret_cast<float*>(smem + F::kRingBytes), bars + warp * F::kStages};
-    w.lane = lane;
-    w.kwarps = 1 << p.kshift;
-    w.rwarps = kWarps >> p.kshift;
-    w.wk = warp & (w.kwarps - 1);
-    w.wr = warp >> p.kshift;
-    w.chunks = (p.kb + Fmt<T>::cb - 1) / Fmt<T>::cb;
-    const int groups = M == kDense ? static_cast<int>((p.N + F::kGroup - 1) / F::kGroup) : L.groups;
-    w.units = groups * p.tiles;
-    w.issue_from(blockIdx.x);
-    w.istage = w.cstage = 0;
-    w.cphase = 0;
+    w.res_shift = 31 - __clz(M == kGateUp ? w.stage_rows / 2 : w.stage_rows);
+    w.sub = M == kGateUp ? max(1, 32 >> w.res_shift) : 1;
+    w.groups = M == kDense ? static_cast<int>((p.N + kFewGroup - 1) / kFewGroup) : L.groups;
+    // consecutive units for each CTA: those of one group follow each other
+    const int64_t total = static_cast<int64_t>(w.groups) * p.units;
+    const int64_t begin = total * blockIdx.x / gridDim.x;
+    Place at{static_cast<int>(begin / p.units), static_cast<int>(begin % p.units),
+             total * (blockIdx.x + 1) / gridDim.x - begin};
+    w.f = at;
+    w.fs = w.fc = w.fslot = 0;
     w.dead = false;
-    // the lists' scratch lies in the ring: its plain accesses come before the copies' writes
-    if (M != kDense) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < F::kStages; ++i) w.issue();
-    griddep_wait();   // activations (and, of kDown, Y and the sums) belong to the kernel before
-    if (M == kDown && groups == 0)
-        for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) w.combine(tile);
-    for (int u = blockIdx.x; u < w.units; u += gridDim.x) {
-        const int n = w.count_of(w.group_of(u));
-        if (n <= F::kGroup / 4)
-            w.template unit<1>(u);
-        else if (n <= F::kGroup / 2)
-            w.template unit<2>(u);
-        else
-            w.template unit<4>(u);
+    for (int i = 0; i < p.stages; ++i) w.fill();
+    griddep_wait();   // activations (and what this kernel writes) belong to the kernels before
+    int slot = 0;
+    uint32_t phase = 0;
+#pragma unroll 1
+    while (at.left > 0) {
+        if (w.count_of(at.gi) <= 4 * (3 - Terms)) {
+            w.template consume<1>(at, slot, phase);
+        } else {
+            if constexpr (Terms == 2) w.template consume<2>(at, slot, phase);
+        }
+    }
+}
+
+// Y[n] = sum_j weights[n][j] part[n][j], over the pairs that have an expert, in the order of j.
+__global__ void __launch_bounds__(256)
+combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
+               const float* __restrict__ weights, int64_t N, int top_k, int E, int D,
+               float* __restrict__ Y) {
+    griddep_wait();   // `part`, and Y, which the kernels before may still read as X
+    const int quads = D / 4;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < N * quads; i += step) {
+        const int64_t n = i / quads;
+        const int r = static_cast<int>(i - n * quads);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t q = n * top_k + j;
+            const int id = ids[q];
+            if (id < 0 || id >= E) continue;
+            const float w = weights[q];
+            const float4 v = reinterpret_cast<const float4*>(part)[q * quads + r];
+            y.x = fmaf(w, v.x, y.x);
+            y.y = fmaf(w, v.y, y.y);
+            y.z = fmaf(w, v.z, y.z);
+            y.w = fmaf(w, v.w, y.w);
+        }
+        float* out = Y + n * D + 4 * r;   // only 4-byte aligned
+        out[0] = y.x;
+        out[1] = y.y;
+        out[2] = y.z;
+        out[3] = y.w;
     }
 }
 
 // ---- Preparation ------------------------------------------------------------------------
 
 // One warp per 32-element block of X: two-term split activations in the order of `type`.
-// Also zeroes the counters of the kernel after next.
 __global__ void __launch_bounds__(256)
 split_kernel(const float* __restrict__ X, int64_t n_blocks, int kb, int type,
-             __half* __restrict__ xb, float2* __restrict__ xm, unsigned* zero, int n_zero) {
+             __half* __restrict__ xb, float2* __restrict__ xm) {
     griddep_launch_dependents();
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_zero; i += blockDim.x) zero[i] = 0u;
     const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int place = few_place(type, lane);
     for (int64_t b = warp; b < n_blocks; b += step) {
-        const float x = X[b * 32 + lane];
-        const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
-        const int e = block_exponent(amax);
-        const float xs = x * pow2f(14 - e);
-        const __half hi = __float2half_rn(xs);
-        const __half lo = __float2half_rn(xs - __half2float(hi));
-        float sum = __half2float(hi) + __half2float(lo);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         const int64_t row = b / kb, blk = b % kb;
-        __half* out = xb + (row * 2 * kb + blk) * 32;
-        out[place] = hi;
-        out[static_cast<int64_t>(kb) * 32 + place] = lo;
-        if (lane == 0) {
-            const float s = pow2f(e - 14);
-            xm[b] = make_float2(s, s * sum);
-        }
+        write_split(X[b * 32 + lane], lane, place, xb + (row * 2 * kb + blk) * 32,
+                    static_cast<int64_t>(kb) * 32, xm + b);
     }
 }
 
@@ -780,48 +805,67 @@ mx_split_kernel(const float* __restrict__ X, int64_t n_blocks, __half* __restric
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 cudaError_t launch_split(const float* X, int64_t rows, int kb, int type, __half* xb, float2* xm,
-                         unsigned* zero, int n_zero, const DeviceInfo* info, cudaStream_t s) {
+                         const DeviceInfo* info, cudaStream_t s) {
     const int64_t blocks = rows * kb;
     const int64_t grid = std::min<int64_t>((blocks + 7) / 8, int64_t(info->sm_count) * 8);
     split_kernel<<<static_cast<unsigned>(std::max<int64_t>(grid, 1)), 256, 0, s>>>(
-        X, blocks, kb, type, xb, xm, zero, n_zero);
+        X, blocks, kb, type, xb, xm);
     return cudaGetLastError();
 }
 
-// How many of a CTA's four warps split K: as many as the chunks allow while the row tiles of
-// four-row-warp CTAs would leave SMs idle. `work`: tiles x groups at 32 rows a warp.
-int pick_kshift(int64_t work, int chunks, int sms) {
-    int ks = 0;
-    while (ks < 2 && (2 << ks) <= chunks && work * (1 << ks) < int64_t(4) * 2 * sms) ++ks;
-    return ks;
-}
-
-template <int T, int M, int Terms>
-cudaError_t launch_few(Params& p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
-    using F = Few<T, M, Terms>;
-    const int chunks = (p.kb + Fmt<T>::cb - 1) / Fmt<T>::cb;
-    const int64_t warp_tiles = (p.rows + 31) / 32;
-    p.kshift = pick_kshift(warp_tiles * groups, chunks, info->sm_count);
-    const int rwarps = kWarps >> p.kshift;
-    p.tiles = static_cast<int>((warp_tiles + rwarps - 1) / rwarps);
-    p.status = info->status;
-    const int64_t units = p.tiles * groups;
-    const unsigned grid = static_cast<unsigned>(std::max<int64_t>(
-        1, std::min<int64_t>(units, int64_t(info->sm_count) * 2)));
-    auto kernel = few_kernel<T, M, Terms>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
-    if (e != cudaSuccess) return e;
+// A launch that may start while the kernel before it on the stream still runs (it waits with
+// griddep_wait).
+template <typename... Sig, typename... Args>
+cudaError_t launch_after(void (*kernel)(Sig...), unsigned grid, int threads, int smem, cudaStream_t s,
+                         const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const Params>(p));
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int T, int M, int Terms>
+cudaError_t launch_few(Params& p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
+    // Chunks of up to 64 blocks (four for each of the 16 consumer warps), of equal size but for
+    // the last; with fewer blocks, fewer warps share a chunk and a stage has more rows.
+    constexpr int kMax = kWarps * kMaxBlocks;
+    constexpr int kUnit = T == GQ_TYPE_Q4_K ? 8 : 1;   // super-blocks stay whole
+    p.chunks = (p.kb + kMax - 1) / kMax;
+    p.kc = ((p.kb + p.chunks - 1) / p.chunks + kUnit - 1) / kUnit * kUnit;
+    p.kwarps = p.kc > kMax / 2 ? kWarps : (p.kc > kMax / 4 ? kWarps / 2 : kWarps / 4);
+    p.per = (p.kc + p.kwarps - 1) / p.kwarps;
+    if (T == GQ_TYPE_Q4_K) p.per = (p.per + 1) / 2 * 2 == 2 ? 2 : 4;   // inside one super-block
+    const int stage_rows = 16 * Fmt<T>::tiles * (kWarps / p.kwarps);
+    const int results = M == kGateUp ? stage_rows / 2 : stage_rows;
+    const int unit_rows = M == kGateUp ? std::max(32, results) : results;
+    p.units = (p.rows + unit_rows - 1) / unit_rows;
+    // A row's words, at an odd multiple of 16 bytes: the eight rows that a warp reads at once
+    // then lie on distinct groups of four banks.
+    p.pitch = (p.kc * Fmt<T>::bb + 15 + 15) / 16 * 16;
+    if (p.pitch % 32 == 0) p.pitch += 16;
+    p.stage_bytes = (stage_rows * p.pitch + 16 + 127) / 128 * 128;   // 16: the last word's second half
+    p.stages = std::min(kMaxStages, (kSmemMax - kRingAt) / p.stage_bytes);
+    p.status = info->status;
+    const unsigned grid = static_cast<unsigned>(
+        std::max<int64_t>(1, std::min<int64_t>(p.units * groups, info->sm_count)));
+    const int smem = kRingAt + p.stages * p.stage_bytes;
+    auto kernel = few_kernel<T, M, Terms>;
+    static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
+    const uint64_t bit = uint64_t(1) << info->device;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_after(kernel, grid, kThreads, smem, s, static_cast<const Params&>(p));
 }
 
 template <int M>
@@ -850,7 +894,7 @@ Params dense_params(const MatProblem& m, int64_t n0, int64_t n) {
 }
 
 struct MoeSpace {   // offsets in the workspace of one launch over n tokens
-    int64_t xb, xm, hb, hm, part, arrived, bytes;
+    int64_t xb, xm, hb, hm, part, bytes;
 };
 
 MoeSpace moe_space(const MoeProblem& m, int64_t n) {
@@ -861,8 +905,7 @@ MoeSpace moe_space(const MoeProblem& m, int64_t n) {
     s.hb = s.xm + align256(n * (m.D / 32) * 8);
     s.hm = s.hb + align256(pairs * m.F * 4);
     s.part = s.hm + align256(pairs * (m.F / 32) * 8);
-    s.arrived = s.part + align256(pairs * m.D * 4);
-    s.bytes = s.arrived + align256((m.D / 32) * 4);
+    s.bytes = s.part + align256(pairs * m.D * 4);
     return s;
 }
 
@@ -881,9 +924,9 @@ int64_t few_workspace_bytes(int64_t K, int64_t N) {
 
 // Tokens of one launch: few enough for the workspace, and for 2^30 units.
 int64_t few_tokens_that_fit(int64_t M, int64_t K, int64_t N, int64_t workspace_bytes) {
-    const int64_t units = std::max<int64_t>(kFewGroup2, (int64_t(1) << 30) / ((M + 31) / 32) * kFewGroup2);
+    const int64_t units = std::max<int64_t>(kFewGroup, (int64_t(1) << 30) / ((M + 31) / 32) * kFewGroup);
     int64_t n = std::min(std::min(N, kFewMaxTokens), units);
-    while (n > 0 && few_workspace_bytes(K, n) > workspace_bytes) n = n > kFewGroup2 ? n / 2 : n - 1;
+    while (n > 0 && few_workspace_bytes(K, n) > workspace_bytes) n = n > kFewGroup ? n / 2 : n - 1;
     return n;
 }
 
@@ -902,9 +945,9 @@ cudaError_t launch_few_mul_mat(const MatProblem& m, int64_t N, void* workspace,
         p.xb = reinterpret_cast<const uint4*>(ws);
         p.xm = reinterpret_cast<const float*>(xm);
         e = launch_split(m.X + n0 * m.K, n, p.kb, GQ_TYPE_MXFP4, reinterpret_cast<__half*>(ws), xm,
-                         nullptr, 0, info, s);
+                         info, s);
         if (e == cudaSuccess)
-            e = launch_few<GQ_TYPE_MXFP4, kDense, 2>(p, (n + kFewGroup2 - 1) / kFewGroup2, info, s);
+            e = launch_few<GQ_TYPE_MXFP4, kDense, 2>(p, (n + kFewGroup - 1) / kFewGroup, info, s);
     }
     return e;
 }
@@ -928,7 +971,7 @@ cudaError_t launch_few_mx4x(const MatProblem& m, int64_t N, void* workspace, cud
         m.X, blocks, reinterpret_cast<__half*>(ws), xm);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_few<GQ_TYPE_MXFP4, kDense, 1>(p, (N + kFewGroup1 - 1) / kFewGroup1, info, s);
+    return launch_few<GQ_TYPE_MXFP4, kDense, 1>(p, (N + kFewGroup - 1) / kFewGroup, info, s);
 }
 
 // ---- Mixture of experts -----------------------------------------------------------------
@@ -947,9 +990,8 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const int64_t n = std::min(per, m.N - n0);
         const MoeSpace at = moe_space(m, n);
         const int pairs = static_cast<int>(n * m.top_k);
-        unsigned* arrived = reinterpret_cast<unsigned*>(ws + at.arrived);
         // groups there can be: every pair its own expert, or full groups over few experts
-        const int64_t groups = std::min<int64_t>(pairs, m.E + pairs / kFewGroup2);
+        const int64_t groups = std::min<int64_t>(pairs, m.E + pairs / kFewGroup);
         Params g{};
         g.W = m.W_gate;
         g.W2 = m.W_up;
@@ -964,7 +1006,6 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         g.top_k = m.top_k;
         g.pairs = pairs;
         g.ids = m.ids + n0 * m.top_k;
-        g.weights = m.weights + n0 * m.top_k;
         g.hb = reinterpret_cast<__half*>(ws + at.hb);
         g.hm = reinterpret_cast<float2*>(ws + at.hm);
         g.h_type = m.t_down;
@@ -977,14 +1018,17 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         d.kb = static_cast<int>(m.F / 32);
         d.xb = reinterpret_cast<const uint4*>(ws + at.hb);
         d.xm = reinterpret_cast<const float*>(ws + at.hm);
-        d.Y = m.Y + n0 * m.D;
         d.part = reinterpret_cast<float*>(ws + at.part);
-        d.arrived = arrived;
         e = launch_split(m.X + n0 * m.D, n, g.kb, m.t, reinterpret_cast<__half*>(ws + at.xb),
-                         reinterpret_cast<float2*>(ws + at.xm), arrived, static_cast<int>(m.D / 32),
-                         info, s);
+                         reinterpret_cast<float2*>(ws + at.xm), info, s);
         if (e == cudaSuccess) e = launch_typed<kGateUp>(m.t, g, groups, info, s);
         if (e == cudaSuccess) e = launch_typed<kDown>(m.t_down, d, groups, info, s);
+        if (e == cudaSuccess) {
+            const int64_t blocks = (n * (m.D / 4) + 255) / 256;
+            e = launch_after(combine_kernel, static_cast<unsigned>(std::min<int64_t>(blocks, info->sm_count * 8)),
+                             256, 0, s, static_cast<const float*>(d.part), g.ids, m.weights + n0 * m.top_k,
+                             n, m.top_k, g.E, d.rows, m.Y + n0 * m.D);
+        }
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

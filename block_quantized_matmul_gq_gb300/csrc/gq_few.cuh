@@ -21,8 +21,7 @@
 
 namespace gq {
 
-constexpr int kFewGroup2 = 16;    // tokens per pass over the weights, two-term activations
-constexpr int kFewGroup1 = 32;    // one-term activations
+constexpr int kFewGroup = 8;   // tokens per pass over the weights
 
 // Place (0..31) of element i of a block in the order in which the four lanes that share a
 // weight row hold it: lane t = place / 8 takes the block's bytes 4t..4t+3 (and 16 + 4t.. for
