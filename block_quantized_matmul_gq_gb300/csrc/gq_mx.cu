@@ -1,15 +1,441 @@
-// gq_mx.cu -- the microscaled mul_mat: MXFP4 weights times X quantized to MXFP4.
-#include "gq_internal.h"
+// gq_mx.cu -- the microscaled mul_mat: MXFP4 weights times X quantized to MXFP4, on the
+// block-scaled tensor cores.
+//
+// Mathematics. Y[n][m] = sum_b 2^(s_w[m][b] + s_x[n][b]) sum_{k in b} w_k x_k over 32-element
+// blocks of E2M1 values. tcgen05.mma kind::mxf4 takes exactly this: packed E2M1 operands, one
+// E8M0 scale per row and block, fp32 accumulators in TMEM. Every product and scale is exact, so
+// the sums are the only roundings. The order of the 32 values inside a block does not matter as
+// long as both sides agree, so the codes keep the file's arrangement (value j beside j + 16) and
+// X is packed likewise: no weight is unpacked anywhere.
+//
+// Two launches. mx_prepare_kernel lays both operands out as the MMA reads them: records of
+// 128 weight rows (kBN token rows) x 256 k, i.e. rows of 128 bytes in the 128-byte swizzle, then
+// the scales as 32-row x 16-byte atoms (row r's four scales at (r % 32) 16 + (r / 32) 4), so that
+// one bulk copy brings a stage's operand. X is quantized on the way. This costs the weights one
+// more read and write (about 0.3 us a MB); laid out inside the product it would be paid again
+// for every token tile, and would put warps between the copies and the MMA.
+//
+// mx_gemm_kernel: one persistent CTA per SM; one thread copies, one issues MMAs (four of K = 64
+// a stage, after the copies of the scales to TMEM), four warps read one accumulator out while
+// the other fills. What bounds it: the fp32 results. At M = 11008, K = 4096, N = 2048 the
+// operands are 29 MB, Y is 90 MB, and the products take 185 GFLOP. Tiles of 128 x 192 because
+// two accumulators of 192 columns and two sets of scales fit TMEM's 512 columns (256 would leave
+// no room to overlap); 44 KB a stage from L2.
+#include <algorithm>
+#include <atomic>
+
+#include "gq_few.cuh"
+#include "gq_umma.cuh"
 
 namespace gq {
+namespace {
 
-int64_t mx4x_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-    (void)M;
-    return few_mx_workspace_bytes(K, N);
+constexpr int kBM = 128;          // weight rows of a tile
+constexpr int kStageK = 256;      // k of a stage: 128 bytes a row
+constexpr int kStageBlocks = kStageK / 32;
+constexpr int kRowBytes = kStageK / 2;
+constexpr int kAtom = 512;        // scales of 128 rows x 4 blocks
+constexpr int kMxThreads = 192;   // producer warp, MMA warp, four epilogue warps
+
+__host__ __device__ constexpr int chunks_of(int rows) { return (rows + 127) / 128; }
+// Bytes of an operand record of `rows` rows: codes, then for each four blocks the atoms.
+__host__ __device__ constexpr int record_bytes(int rows) { return rows * kRowBytes + 2 * chunks_of(rows) * kAtom; }
+
+template <int BN>
+struct Mx {
+    static constexpr int kA = record_bytes(kBM), kB = record_bytes(BN);
+    static constexpr int kStage = kA + kB;
+    static constexpr int kStages = 5;
+    static constexpr int kSmem = kStages * kStage + 1024;   // stages on 1024-byte boundaries
+    // TMEM columns: two accumulators, then two sets of scales (8 for A, 8 or 16 for B)
+    static constexpr int kScales = 2 * BN, kScaleSet = 8 + 8 * chunks_of(BN);
+    static constexpr int kColumns = 2 * BN + 2 * kScaleSet <= 256 ? 256 : 512;
+    static_assert(2 * BN + 2 * kScaleSet <= 512 && kStage % 1024 == 0 && kA % 1024 == 0, "layout");
+};
+
+// ---- Preparation ------------------------------------------------------------------------
+
+// Where the 16 code bytes of block j (0..7) of row r lie in a record, and its scale.
+__device__ __forceinline__ int code_at(int r, int j) { return r * kRowBytes + ((j ^ (r & 7)) << 4); }
+__device__ __forceinline__ int scale_at(int rows, int r, int j) {
+    return rows * kRowBytes + ((j >> 2) * chunks_of(rows) + (r >> 7)) * kAtom + (r & 31) * 16 +
+           ((r >> 5) & 3) * 4 + (j & 3);
 }
 
-cudaError_t launch_mx4x(const MatProblem& p, int64_t N, void* workspace, cudaStream_t s) {
-    return launch_few_mx4x(p, N, workspace, s);
+struct PrepareParams {
+    const uint8_t* W;
+    const float* X;
+    uint8_t* wrec;       // [row tile][k tile]
+    uint8_t* xrec;
+    int64_t M, N;
+    int kb, ktiles;      // blocks of a row; 256-k tiles
+    int bn;
+    int64_t w_ctas;      // CTAs that lay out weights; the others quantize X
+    int64_t w_blocks, x_blocks;   // padded blocks of either
+};
+
+// Weights: one thread per 17-byte block. X: four lanes per block (lane q: elements 4q..4q+3 and
+// 16+4q..), as in the quantizer. Rows and k that pad a record are zeros with scale 2^0.
+__global__ void __launch_bounds__(256) mx_prepare_kernel(const __grid_constant__ PrepareParams p) {
+    griddep_launch_dependents();
+    const int kpad = p.ktiles * kStageBlocks;
+    if (blockIdx.x < p.w_ctas) {
+        const int64_t total = p.M * p.kb * kMxfp4Bytes;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.w_blocks;
+             i += p.w_ctas * 256) {
+            const int64_t row = i / kpad;
+            const int kb = static_cast<int>(i - row * kpad);
+            uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t scale = 127;
+            if (row < p.M && kb < p.kb) {
+                const int64_t at = (row * p.kb + kb) * kMxfp4Bytes, from = at & ~int64_t(3);
+                uint32_t w[6];
+#pragma unroll
+                for (int k = 0; k < 5; ++k) {
+                    if (from + 4 * k + 4 <= total) {
+                        w[k] = *reinterpret_cast<const uint32_t*>(p.W + from + 4 * k);
+                    } else {   // the matrix ends inside this word
+                        w[k] = 0;
+                        for (int b = 0; b < 4; ++b)
+                            if (from + 4 * k + b < total) w[k] |= uint32_t(p.W[from + 4 * k + b]) << (8 * b);
+                    }
+                }
+                w[5] = 0;
+                // bytes 1..16 of the block: `sh` bits into the words
+                const uint32_t lead = static_cast<uint32_t>(at - from);
+                scale = (w[0] >> (8 * lead)) & 0xFFu;
+                const uint32_t sh = 8 * (lead + 1);
+                if (sh == 32) {
+                    codes = make_uint4(w[1], w[2], w[3], w[4]);
+                } else {
+                    codes = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+                }
+            }
+            const int r = static_cast<int>(row & (kBM - 1)), j = kb & 7;
+            uint8_t* rec = p.wrec + ((row >> 7) * p.ktiles + (kb >> 3)) * static_cast<int64_t>(record_bytes(kBM));
+            *reinterpret_cast<uint4*>(rec + code_at(r, j)) = codes;
+            rec[scale_at(kBM, r, j)] = static_cast<uint8_t>(scale);
+        }
+        return;
+    }
+    const int q = threadIdx.x & 3;
+    const int64_t x_ctas = gridDim.x - p.w_ctas;
+    const int64_t steps = (p.x_blocks + 63) / 64;
+    for (int64_t s = blockIdx.x - p.w_ctas; s < steps; s += x_ctas) {
+        const int64_t i = s * 64 + (threadIdx.x >> 2);
+        const int64_t row = i / kpad;
+        const int kb = static_cast<int>(i - row * kpad);
+        const bool real = i < p.x_blocks && row < p.N && kb < p.kb;
+        float v[8] = {};
+        if (real) {
+            const float* src = p.X + (row * p.kb + kb) * 32 + 4 * q;   // only 4-byte aligned
+            if ((reinterpret_cast<uintptr_t>(p.X) & 15) == 0) {
+                const float4 a = *reinterpret_cast<const float4*>(src);
+                const float4 b = *reinterpret_cast<const float4*>(src + 16);
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = src[k];
+                    v[4 + k] = src[16 + k];
+                }
+            }
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        if (i >= p.x_blocks) continue;
+        const uint32_t byte = real ? mx_scale_byte(amax) : 127u;
+        uint32_t codes = 0;
+        if (real && byte != 255) {
+            const float inv = mx_inverse_scale(byte);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t c = e2m1_code(fabsf(v[k]) * inv) | ((__float_as_uint(v[k]) >> 31) << 3);
+                codes |= c << (k < 4 ? 8 * k : 8 * (k - 4) + 4);
+            }
+        }
+        const int tile = static_cast<int>(row / p.bn), r = static_cast<int>(row - int64_t(tile) * p.bn), j = kb & 7;
+        uint8_t* rec = p.xrec + (static_cast<int64_t>(tile) * p.ktiles + (kb >> 3)) * record_bytes(p.bn);
+        *reinterpret_cast<uint32_t*>(rec + code_at(r, j) + 4 * q) = codes;
+        if (q == 0) rec[scale_at(p.bn, r, j)] = static_cast<uint8_t>(byte);
+    }
+}
+
+// ---- Product ----------------------------------------------------------------------------
+
+// Instruction descriptor, kind::mxf4: A and B E2M1 (1 at bits 7 and 10), N >> 3 at [17,23),
+// E8M0 scales (bit 23), M >> 4 at [24,29), K = 64 (bit 31 = 0); which of a word's four scale bytes
+// belong to the instruction's two blocks: 0 or 2, for B at [4,6) and for A at [29,31).
+__host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int sf) {
+    return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24) |
+           (static_cast<uint32_t>(sf) << 29);
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// One atom of scales (32 rows x 16 bytes, 8-row groups 128 bytes apart, no swizzle) to four TMEM
+// columns, repeated in the four 32-lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+    const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
+                          (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+struct GemmParams {
+    const uint8_t* wrec;
+    const uint8_t* xrec;
+    float* Y;
+    int64_t M, N;
+    int ktiles, m_tiles, n_tiles;
+    unsigned* status;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using C = Mx<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_at;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_addr(&full[i]), 1);
+            mbar_init(smem_addr(&empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&acc_full[i]), 1);
+            mbar_init(smem_addr(&acc_empty[i]), 4);
+        }
+        mbar_init(smem_addr(&drained), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&tmem_at), C::kColumns);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    griddep_wait();   // the records; and Y may still be in use before
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int slot = 0;
+            uint32_t phase = 1;   // of `empty`: the first round passes at once
+            int used = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const int64_t mt = t / p.n_tiles, nt = t % p.n_tiles;
+                const uint8_t* a = p.wrec + mt * p.ktiles * static_cast<int64_t>(C::kA);
+                const uint8_t* b = p.xrec + nt * p.ktiles * static_cast<int64_t>(C::kB);
+                for (int k = 0; k < p.ktiles; ++k) {
+                    ok = mbar_wait(smem_addr(&empty[slot]), phase);
+                    if (!ok) break;
+                    const uint32_t bar = smem_addr(&full[slot]), dst = ring + slot * C::kStage;
+                    mbar_arrive_expect_tx(bar, C::kStage);
+                    bulk_g2s(dst, a + static_cast<int64_t>(k) * C::kA, C::kA, bar);
+                    bulk_g2s(dst + C::kA, b + static_cast<int64_t>(k) * C::kB, C::kB, bar);
+                    ++used;
+                    if (++slot == C::kStages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) report_status(p.status, kStatusTimeout);
+            // no copy may be in flight when the CTA leaves
+            for (int i = 0; i < min(used, C::kStages); ++i) {
+                if (--slot < 0) {
+                    slot = C::kStages - 1;
+                    phase ^= 1;
+                }
+                mbar_wait(smem_addr(&full[slot]), phase ^ 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int slot = 0, n_tile = 0;
+            uint32_t phase = 0, set = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n_tile) {
+                const int buf = n_tile & 1;
+                ok = mbar_wait(smem_addr(&acc_empty[buf]), (n_tile >> 1 & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * BN;
+                for (int k = 0; k < p.ktiles; ++k) {
+                    ok = mbar_wait(smem_addr(&full[slot]), phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = ring + slot * C::kStage, b = a + C::kA;
+                    const uint32_t sfa = tmem + C::kScales + set * C::kScaleSet, sfb = sfa + 8;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        copy_scales(sfa + 4 * g, a + kBM * kRowBytes + g * kAtom);
+#pragma unroll
+                        for (int c = 0; c < chunks_of(BN); ++c)
+                            copy_scales(sfb + 4 * (chunks_of(BN) * g + c),
+                                        b + BN * kRowBytes + (chunks_of(BN) * g + c) * kAtom);
+                    }
+                    const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // 32 bytes of a row each
+                        umma_mxf4(d, ad + 2 * i, bd + 2 * i, i & 1 ? mx_idesc(kBM, BN, 2) : mx_idesc(kBM, BN, 0),
+                                  sfa + 4 * (i >> 1), sfb + 4 * chunks_of(BN) * (i >> 1), k > 0 || i > 0);
+                    umma_commit(smem_addr(&empty[slot]));
+                    set ^= 1;
+                    if (++slot == C::kStages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) umma_commit(smem_addr(&acc_full[buf]));
+            }
+            if (!ok) report_status(p.status, kStatusTimeout);
+            umma_commit(smem_addr(&drained));   // nothing may run when TMEM is given back
+            mbar_wait(smem_addr(&drained), 0);
+        }
+    } else {
+        const int quarter = warp & 3;   // the TMEM lanes that this warp may read
+        int n_tile = 0;
+        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n_tile) {
+            const int buf = n_tile & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&acc_full[buf]), n_tile >> 1 & 1))) {
+                report_status(p.status, kStatusTimeout);
+                break;
+            }
+            tc_fence_after();
+            const int64_t m = (t / p.n_tiles) * kBM + quarter * 32 + lane, n0 = (t % p.n_tiles) * BN;
+            const int n_left = static_cast<int>(min(static_cast<int64_t>(BN), p.N - n0));
+            const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+            float* out = p.Y + n0 * p.M + m;
+            // 32 columns (tokens) at a time: each store is 128 consecutive bytes of a token's row
+            for (int c = 0; c < BN; c += 32) {
+                if (c >= n_left) break;
+                uint32_t r[32];
+                tmem_ld16_async(src + c, r);
+                tmem_ld16_async(src + c + 16, r + 16);
+                tmem_ld_wait();
+                if (m < p.M) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < n_left) __stcs(out + (c + i) * p.M, __uint_as_float(r[i]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[buf]));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::kColumns);
+}
+
+// ---- Host side --------------------------------------------------------------------------
+
+constexpr int64_t kMxMinTokens = 17;   // below, the few-token kernel
+
+int bn_for(int64_t N) { return N <= 64 ? 64 : (N <= 128 ? 128 : 192); }
+
+struct MxSpace {
+    int64_t m_tiles, n_tiles, ktiles, w_bytes, x_bytes;
+};
+
+MxSpace mx_space(int64_t M, int64_t K, int64_t N) {
+    const int bn = bn_for(N);
+    MxSpace s{};
+    s.m_tiles = (M + kBM - 1) / kBM;
+    s.n_tiles = (N + bn - 1) / bn;
+    s.ktiles = (K + kStageK - 1) / kStageK;
+    s.w_bytes = s.m_tiles * s.ktiles * record_bytes(kBM);
+    s.x_bytes = s.n_tiles * s.ktiles * record_bytes(bn);
+    return s;
+}
+
+template <int BN>
+cudaError_t launch_mx_gemm(const GemmParams& g, const DeviceInfo* info, cudaStream_t s) {
+    auto kernel = mx_gemm_kernel<BN>;
+    static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
+    const uint64_t bit = uint64_t(1) << info->device;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Mx<BN>::kSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, info->sm_count)));
+    cfg.blockDim = dim3(kMxThreads);
+    cfg.dynamicSmemBytes = Mx<BN>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, g);
+}
+
+}  // namespace
+
+int64_t mx4x_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+    if (N < kMxMinTokens) return few_mx_workspace_bytes(K, N);
+    const MxSpace s = mx_space(M, K, N);
+    return s.w_bytes + s.x_bytes;   // records are multiples of 1024 bytes
+}
+
+cudaError_t launch_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStream_t s) {
+    if (N < kMxMinTokens) return launch_few_mx4x(m, N, workspace, s);
+    DeviceInfo* info = nullptr;
+    cudaError_t e = current_device_info(&info);
+    if (e != cudaSuccess) return e;
+    const MxSpace at = mx_space(m.M, m.K, N);
+    if (at.m_tiles > 0x7FFFFFFF || at.n_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PrepareParams p{};
+    p.W = m.W;
+    p.X = m.X;
+    p.wrec = ws;
+    p.xrec = ws + at.w_bytes;
+    p.M = m.M;
+    p.N = N;
+    p.kb = static_cast<int>(m.K / 32);
+    p.ktiles = static_cast<int>(at.ktiles);
+    p.bn = bn_for(N);
+    p.w_blocks = at.m_tiles * kBM * at.ktiles * kStageBlocks;
+    p.x_blocks = at.n_tiles * p.bn * at.ktiles * kStageBlocks;
+    const int64_t most = int64_t(info->sm_count) * 8;
+    p.w_ctas = std::min<int64_t>((p.w_blocks + 255) / 256, most);
+    const int64_t x_ctas = std::min<int64_t>((p.x_blocks + 63) / 64, most);
+    mx_prepare_kernel<<<static_cast<unsigned>(p.w_ctas + x_ctas), 256, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const GemmParams g{p.wrec, p.xrec, m.Y, m.M, N, p.ktiles, static_cast<int>(at.m_tiles),
+                       static_cast<int>(at.n_tiles), info->status};
+    switch (p.bn) {
+        case 64: return launch_mx_gemm<64>(g, info, s);
+        case 128: return launch_mx_gemm<128>(g, info, s);
+        default: return launch_mx_gemm<192>(g, info, s);
+    }
 }
 
 }  // namespace gq
