@@ -3,30 +3,32 @@
 //
 // Mathematics. A weight row's block is d (q - z) with small integers q (or E2M1 values), so
 //     sum_k What[m][k] x[k] = sum_b d_b s_b sum_{k in b} (q_k - z) xs_k
-// with xs = x / s_b split in two fp16 terms (gq_few.cuh). The inner sum runs on the tensor
-// cores: mma.m16n8k16 with 16 weight rows as exact fp16 codes, 8 columns = 4 tokens x (hi, lo),
-// two instructions a block, fp32 accumulators; the outer sum is one fp32
-// multiply-add per block, row and token. Nothing is rounded below 22 bits but the fp32 sums.
+// with xs = x / s split in two fp16 terms (gq_few.cuh). The inner sum runs on the tensor
+// cores: mma.m16n8k16 with 16 weight rows as exact fp16 codes and 8 tokens as columns, four
+// instructions a block (two halves of k, hi and lo into the same fp32 accumulators); the outer
+// sum is one fp32 multiply-add per block, row and token. Nothing is rounded below 22 bits but
+// the fp32 sums.
 //
-// What bounds it. One pass over the weights: at most 34 bytes per 32 weights from DRAM, about
-// 30 instructions per 16 rows x 32 weights x 4 tokens. At 6.8 TB/s an SM takes in 512 4-bit
-// weights every 12 cycles, 47 issue slots, so instructions come close to memory as the limit;
-// that is why codes become fp16 by masks alone (subnormals, gq_few.cuh) and why tcgen05 is not
-// used here: its operands would have to pass through shared memory once more, with the
-// scales applied there, and its 128-row tiles leave most SMs without work at these sizes.
+// What bounds it. One pass over the weights: 17 to 34 bytes per 32 weights from DRAM, about 40
+// instructions per 16 rows x 32 weights x 8 tokens. At 6.8 TB/s an SM takes in 512 4-bit weights
+// every 12 cycles, 47 issue slots, so instructions come before memory as the limit, and with
+// them the instruction cache: forms of this kernel with all loops unrolled (70 to 150 KB of
+// code) took 4 to 10 us for a stage that this one ends in one. Loops here stay rolled, what is
+// rare is not inlined, and the number of column tiles is the kernel's, not a branch's. tcgen05
+// is not used: its operands would have to pass through shared memory once more, the scales
+// would have to be applied outside, and its 128-row tiles leave most SMs without work here.
 //
-// Layout of the work. One persistent CTA per SM, 16 warps, and a ring of stages, each some weight
-// rows x up to 64 blocks of K, one bulk copy per row: runs of about a kilobyte, which is what DRAM pages and the copy engine want (16-
-// byte cp.async in 136-byte runs reached 3.3 TB/s, bulk copies of 136 bytes 1.6). A row's copy
-// starts at the 16-byte word that holds its first byte, because rows of 17- and 18-byte blocks
-// start anywhere; words are aligned in registers. The warps split a stage's K range
-// (kwarps), four blocks of 32 rows each, so that the activations of those four blocks stay in
-// registers from stage to stage; then their sums join through shared memory in a fixed order, and the
-// barrier of that join frees the stage for its refill.
-// The ring runs on across units, and weights do not depend on the kernel before, so they start
-// to stream before griddepcontrol.wait.
+// Layout of the work. A unit is (a group of up to 8 NT tokens, 32 result rows); a row warp has a
+// run of consecutive units, so that those of one group follow each other and share activations
+// through L1. Where there are too few units, 2, 4 or 8 warps split a unit's K and join through
+// shared memory in a fixed order; they wait for each other, nobody else does. Every warp runs
+// its own ring of 16-byte asynchronous copies, four lanes to a weight row: a row's chunk from
+// the word that holds its first byte, because rows of 17- and 18-byte blocks start anywhere; the
+// words are aligned in registers. The ring runs on across units, and weights do not depend on
+// the kernel before, so they start to stream before griddepcontrol.wait.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstddef>
 
 #include "gq_few.cuh"
@@ -34,32 +36,35 @@
 namespace gq {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxBlocks = 4;              // of one warp and stage
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 2;
 
 constexpr int64_t kFewMaxTokens = 4096;   // of one launch: bounds the workspace
 
 enum Mode { kDense = 0, kGateUp = 1, kDown = 2 };
 
 template <int T>
-struct Fmt;   // bytes of 32 weights, and the 16-row tiles that a consumer warp takes of a stage
+struct Fmt;   // bytes of 32 weights, blocks per chunk, shared-memory pitch of a row's chunk
 template <>
 struct Fmt<GQ_TYPE_Q4_0> {
-    static constexpr int bb = kQ4Bytes, tiles = 2;
+    static constexpr int bb = kQ4Bytes, cb = 8, pitch = 176;
 };
 template <>
 struct Fmt<GQ_TYPE_Q8_0> {
-    static constexpr int bb = kQ8Bytes, tiles = 1;   // twice the bytes: the same stage
+    static constexpr int bb = kQ8Bytes, cb = 4, pitch = 176;
 };
 template <>
 struct Fmt<GQ_TYPE_Q4_K> {   // a super-block's bytes over its 8 sub-blocks
-    static constexpr int bb = kQ4KBytes / 8, tiles = 2;
+    static constexpr int bb = kQ4KBytes / 8, cb = 8, pitch = 144;
 };
 template <>
 struct Fmt<GQ_TYPE_MXFP4> {
-    static constexpr int bb = kMxfp4Bytes, tiles = 2;
+    static constexpr int bb = kMxfp4Bytes, cb = 8, pitch = 176;
 };
+// Pitches: a chunk is 136 or 144 bytes and starts up to 15 bytes into its first 16-byte word;
+// 176 = 44 words puts the eight rows that a warp reads at once on eight distinct groups of four
+// banks, as 144 = 36 words does where rows are always aligned (Q4_K).
 
 struct Params {
     const uint8_t* W;
@@ -68,25 +73,29 @@ struct Params {
     int64_t row_bytes;
     int rows;                 // weight rows (of one expert)
     int kb;                   // 32-weight blocks per row
-    int kc;                   // blocks of one stage (chunk) of a row
-    int chunks;               // ceil(kb / kc)
-    int kwarps;               // consumer warps that split a chunk, `per` blocks each
-    int per;
-    int units;                // of one group: row tiles of unit_rows
-    int pitch, stage_bytes;   // of a staged row, of a stage
-    int stages;
-    const uint4* xb;          // split activations, 64 bytes per (row, term, block)
-    const float* xm;          // their block factors: float2 (two terms) or float (one)
-    int64_t N;                // tokens
+    int chunks;
+    int tiles;                // 32-row tiles: ceil(rows / 32)
+    int kshift;               // log2 of the warps that split a unit's K
+    const uint4* xb;          // split activations, 64 bytes per (row, block, term)
+    const float* xs;          // their scales: per row (two terms but for kDown), else per block
+    const float* xsum;        // Q4_K: their sums per block
+    int N;                    // tokens
     int E, top_k, pairs;
     const int* ids;
-    float* Y;                 // kDense
+    float* out;               // kDense: Y; kDown: [pair][rows]
     __half* hb;               // kGateUp: split activations of the result,
-    float2* hm;
+    float* hs;                //          scales and sums per block
+    float* hsum;
     int h_type;               //          in the order of the down matrices' type
-    float* part;              // kDown: [pair][rows]
-    unsigned* status;
 };
+
+// 16 bytes global -> shared, of which the first n (1..16) are read and the others zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -109,6 +118,15 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(a));
     return v;
+}
+
+// 32 bytes at once: the two terms of a lane's eight activations. A warp's eight tokens are eight
+// cache lines, and 16-byte loads of hi and lo would visit each twice.
+__device__ __forceinline__ void load32(uint4 (&v)[2], const uint4* at) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+                   "=r"(v[1].z), "=r"(v[1].w)
+                 : "l"(at));
 }
 
 // c = A (16 weight rows x 16) . B (16 x 8 columns), then c += for the block's second half.
@@ -186,43 +204,47 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
 // One block's activations in this lane.
 template <int NT, int Terms>
 struct Columns {
-    uint4 b[NT];               // eight fp16 of column g
-    float2 m[NT];              // {scale, sum} of token t (two terms), scales of 2t, 2t + 1 (one)
+    uint4 b[NT][Terms];        // eight fp16 of column g, hi and lo
+    float2 s[NT], sum[NT];     // scales and sums of tokens 2t, 2t + 1, where there are any
 };
 
-// Products of one 16-row tile with one block, for NT column tiles: tot += d_row s_token (codes
-// . columns), less m_row sum_token for Q4_K. tot: [column tile][rows g, g + 8][tokens].
-template <int T, int Terms, int NT>
+// Products of one 16-row tile with one block, for NT tiles of 8 tokens: tot += d_row s_token
+// (codes . columns), less m_row sum_token for Q4_K. tot: rows g, g + 8 x tokens 2t, 2t + 1.
+template <int T, int Terms, int NT, bool Scaled>
 __device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const float (&d)[2],
                                                const float (&m)[2], const Columns<NT, Terms>& col,
-                                               float (&tot)[NT][2][3 - Terms]) {
+                                               float (&tot)[NT][4]) {
     float c[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n].x, col.b[n].y);
+        mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][0].x, col.b[n][0].y);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n].z, col.b[n].w);
+        mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][0].z, col.b[n][0].w);
+    if constexpr (Terms == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            mma_next(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][1].x, col.b[n][1].y);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][1].z, col.b[n][1].w);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (Terms == 2) {
-                tot[n][h][0] = fmaf(d[h] * col.m[n].x, c[n][2 * h] + c[n][2 * h + 1], tot[n][h][0]);
-                if constexpr (T == GQ_TYPE_Q4_K) tot[n][h][0] = fmaf(-m[h], col.m[n].y, tot[n][h][0]);
-            } else {
-                tot[n][h][0] = fmaf(d[h] * col.m[n].x, c[n][2 * h], tot[n][h][0]);
-                tot[n][h][1] = fmaf(d[h] * col.m[n].y, c[n][2 * h + 1], tot[n][h][1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float s = Scaled ? (i & 1 ? col.s[n].y : col.s[n].x) : 1.0f;
+            tot[n][i] = fmaf(Scaled ? d[i >> 1] * s : d[i >> 1], c[n][i], tot[n][i]);
+            if constexpr (T == GQ_TYPE_Q4_K)
+                tot[n][i] = fmaf(-m[i >> 1], i & 1 ? col.sum[n].y : col.sum[n].x, tot[n][i]);
         }
 }
 
-// The shared lists of a launch over experts: pairs sorted by expert, and groups of up to
-// kFewGroup pairs of one expert.
+// The shared lists of a launch over experts: pairs sorted by expert, and groups of pairs of one
+// expert.
 struct Lists {
-    uint16_t pair[kMoeMaxPairs];
-    uint16_t expert[kMoeMaxPairs];
-    uint16_t start[kMoeMaxPairs];
+    uint16_t pair[kMoeMaxPairs], token[kMoeMaxPairs];
+    uint16_t expert[kMoeMaxPairs], start[kMoeMaxPairs];
     uint8_t count[kMoeMaxPairs];
     int groups;
 };
@@ -230,20 +252,24 @@ struct Lists {
 // Sorts the pairs by expert, in their own order inside an expert: every CTA has to find the
 // same groups. ids outside [0, E) are in no group. `scratch`: kMoeMaxExperts + kMoeMaxPairs
 // ints. One warp ranks 32 pairs at a time by matching their ids; 512 pairs are 16 steps.
-__device__ void build_lists(const Params& p, Lists& L, int* scratch) {
+__device__ __noinline__ void build_lists(const int* __restrict__ all_ids, int E, int top_k, int pairs, int group,
+                                         Lists& L, int* scratch) {
     int* count = scratch;
     int* ids = scratch + kMoeMaxExperts;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) count[e] = 0;
-    for (int q = threadIdx.x; q < p.pairs; q += kThreads) {
-        const int id = p.ids[q];
-        ids[q] = id >= 0 && id < p.E ? id : -1;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
+#pragma unroll 1
+    for (int q = threadIdx.x; q < pairs; q += kThreads) {
+        const int id = all_ids[q];
+        ids[q] = id >= 0 && id < E ? id : -1;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
         const unsigned below = (1u << threadIdx.x) - 1u;
-        for (int q0 = 0; q0 < p.pairs; q0 += 32) {
+#pragma unroll 1
+        for (int q0 = 0; q0 < pairs; q0 += 32) {
             const int q = q0 + threadIdx.x;
-            const int id = q < p.pairs ? ids[q] : -1;
+            const int id = q < pairs ? ids[q] : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
             const int before = id >= 0 ? count[id] : 0;
             __syncwarp();
@@ -253,15 +279,13 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
             }
             __syncwarp();
         }
-    }
-    __syncthreads();
-    // exclusive sums over the experts: pairs (low half) and groups (high half)
-    if (threadIdx.x < 32) {
+        // exclusive sums over the experts: pairs (low half) and groups (high half)
         int base = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + threadIdx.x;
-            const int c = e < p.E ? count[e] : 0;
-            const int g = (c + kFewGroup - 1) / kFewGroup;
+            const int c = e < E ? count[e] : 0;
+            const int g = (c + group - 1) / group;
             int incl = c | (g << 16);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -270,556 +294,564 @@ __device__ void build_lists(const Params& p, Lists& L, int* scratch) {
             }
             const int excl = base + incl - (c | (g << 16));
             const int pair0 = excl & 0xFFFF, group0 = excl >> 16;
+#pragma unroll 1
             for (int i = 0; i < g; ++i) {
                 L.expert[group0 + i] = static_cast<uint16_t>(e);
-                L.start[group0 + i] = static_cast<uint16_t>(pair0 + i * kFewGroup);
-                L.count[group0 + i] = static_cast<uint8_t>(min(kFewGroup, c - i * kFewGroup));
+                L.start[group0 + i] = static_cast<uint16_t>(pair0 + i * group);
+                L.count[group0 + i] = static_cast<uint8_t>(min(group, c - i * group));
             }
-            if (e < p.E) count[e] = pair0;
+            if (e < E) count[e] = pair0;
             base += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
         if (threadIdx.x == 0) L.groups = base >> 16;
     }
     __syncthreads();
-    for (int q = threadIdx.x; q < p.pairs; q += kThreads)
-        if (ids[q] >= 0) L.pair[count[ids[q] & 0xFFFF] + (ids[q] >> 16)] = static_cast<uint16_t>(q);
+#pragma unroll 1
+    for (int q = threadIdx.x; q < pairs; q += kThreads)
+        if (ids[q] >= 0) {
+            const int at = count[ids[q] & 0xFFFF] + (ids[q] >> 16);
+            L.pair[at] = static_cast<uint16_t>(q);
+            L.token[at] = static_cast<uint16_t>(q / top_k);
+        }
     __syncthreads();
 }
 
-// One warp writes a block of a split activation row: lane i holds element i. `xb` and `xm` are
-// the row's places of this block; `lo_at` the distance from hi to lo.
-__device__ __forceinline__ void write_split(float x, int lane, int place, __half* xb, int64_t lo_at,
-                                            float2* xm) {
-    const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
-    const int e = block_exponent(amax);
-    const float xs = x * pow2f(14 - e);
-    const __half hi = __float2half_rn(xs);
-    const __half lo = __float2half_rn(xs - __half2float(hi));
-    float sum = __half2float(hi) + __half2float(lo);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    xb[place] = hi;
-    xb[lo_at + place] = lo;
-    if (lane == 0) {
-        const float s = pow2f(e - 14);
-        *xm = make_float2(s, s * sum);
+// The split of one block of an activation row, held by a warp or by 8 lanes of it: scale
+// exponent of a maximum over them, and an element's two terms.
+struct Split {
+    __half hi, lo;
+    __device__ __forceinline__ Split(float x, int e) {
+        const float xs = x * pow2f(14 - e);
+        hi = __float2half_rn(xs);
+        lo = __float2half_rn(xs - __half2float(hi));
     }
-}
-
-// Shared memory: the lists (and, of kGateUp, the hidden values of a unit), the consumers' sums,
-// the ring.
-constexpr int kSumFloats = 2 * kWarps * 32 * (kFewGroup + 1);   // two halves, in turn
-constexpr int kHiddenFloats = 64 * (kFewGroup + 1);
-constexpr int kListBytes = (static_cast<int>(sizeof(Lists)) + 127) / 128 * 128;
-constexpr int kRingAt = kListBytes + (kSumFloats + kHiddenFloats) * 4;
-constexpr int kMaxStages = 5;
-constexpr int kSmemMax = 227 * 1024 - 512;   // 512: the barriers and what else is static
-static_assert(kRingAt % 128 == 0 && (kMoeMaxExperts + kMoeMaxPairs) * 4 <= kSumFloats * 4,
-              "the lists' scratch lies in the sums");
-
-// A unit: group, row tile, and how many this CTA has from here on.
-struct Place {
-    int gi, tile;
-    int64_t left;
-    __device__ __forceinline__ void next(int units) {
-        --left;
-        if (++tile == units) {
-            tile = 0;
-            ++gi;
-        }
-    }
+    __device__ __forceinline__ float sum() const { return __half2float(hi) + __half2float(lo); }
 };
 
-template <int T, int M, int Terms>
+template <int T, int M, int Terms, int NT>
 struct Worker {
-    static constexpr int kTiles = Fmt<T>::tiles;
-    static constexpr int kBB = Fmt<T>::bb;
+    static constexpr int kBB = Fmt<T>::bb, kCB = Fmt<T>::cb, kPitch = Fmt<T>::pitch;
+    static constexpr int kStageBytes = 32 * kPitch + 16;      // the last word's second half
+    static constexpr int kWords = T == GQ_TYPE_Q4_K ? 9 : 10;   // 16-byte words of a row's chunk
+    static constexpr int kGroup = 8 * NT;
+    static constexpr bool kScaled = M == kDown || Terms == 1;   // scales per block, not per row
+    static constexpr bool kSums = T == GQ_TYPE_Q4_K;
+    static constexpr int kSub = M == kGateUp ? 2 : 1;   // a unit's passes: 16 gate and 16 up rows each
+    static constexpr int kTotals = 2 * NT * 4;   // a lane's, of one pass
+    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kSumBytes = kWarps * kTotals * 32 * 4;
+    static constexpr int kListBytes = M == kDense ? 0 : static_cast<int>(sizeof(Lists));
+    static constexpr int kSmem = kRingBytes + kSumBytes + kListBytes;
+    static_assert((kMoeMaxExperts + kMoeMaxPairs) * 4 <= kRingBytes, "the lists' scratch lies in the ring");
+    using Cols = Columns<NT, Terms>;
+
     const Params& p;
     const Lists& L;
-    float* sums;
-    float* hidden;
-    uint32_t ring, full;          // shared addresses
-    int lane, warp;
-    int stage_rows;               // staged rows
-    int sub;                      // stages of a unit and chunk (kGateUp: a unit is whole 32-blocks)
-    int res_shift;                // log2 of a stage's result rows
-    int groups;
-    Place f;                      // the next stage to fill: unit,
-    int fs, fc, fslot;            // stage in it, chunk; slot
-    bool dead;
+    uint32_t ring;      // this warp's, shared address
+    float* sums;        // the CTA's
+    int lane, wk, wr, kwarps;
+    // the next chunk to copy: unit (group, tile, how many are left), pass, chunk; stage
+    int fgi, ftile, fleft, fs, fc, fstage;
+    int64_t frow;       // its first weight row
 
     __device__ __forceinline__ int expert_of(int gi) const { return M == kDense ? 0 : L.expert[gi]; }
     __device__ __forceinline__ int count_of(int gi) const {
-        if (M != kDense) return L.count[gi];
-        return static_cast<int>(min(static_cast<int64_t>(kFewGroup),
-                                    p.N - static_cast<int64_t>(gi) * kFewGroup));
+        return M == kDense ? min(kGroup, p.N - gi * kGroup) : L.count[gi];
     }
     // activation row of column token i of a group
-    __device__ __forceinline__ int64_t x_row(int gi, int i) const {
-        if (M == kDense) return static_cast<int64_t>(gi) * kFewGroup + i;
-        const int q = L.pair[L.start[gi] + i];
-        return M == kGateUp ? q / p.top_k : q;
-    }
-    // Result rows of a stage; a kGateUp tile is 8 gate rows and the 8 up rows of the same numbers.
-    __device__ __forceinline__ int first_row(int tile, int s) const { return (tile * sub + s) << res_shift; }
-    __device__ __forceinline__ static int row_in_stage(int sr) {
-        return M == kGateUp ? (sr >> 4) * 8 + (sr & 7) : sr;
+    __device__ __forceinline__ int x_row(int gi, int i) const {
+        if (M == kDense) return gi * kGroup + i;
+        return M == kGateUp ? L.token[L.start[gi] + i] : L.pair[L.start[gi] + i];
     }
 
-    // ---- copies ----
+    __device__ __forceinline__ void copy_row() {
+        frow = static_cast<int64_t>(expert_of(fgi)) * p.rows + ftile * 32 + fs * 16;
+    }
 
-    // Starts the copies of the next stage, if there is one: warp w copies rows w, w + 16, ... of
-    // up to 128, a lane each. Every row arrives once on the stage's barrier.
-    __device__ __forceinline__ void fill() {
-        if (f.left == 0) return;
-        const int sr = warp + kWarps * lane;
-        if (sr < stage_rows) {
-            const uint32_t dst = ring + fslot * p.stage_bytes + sr * p.pitch;
-            const uint32_t bar = full + 8 * fslot;
-            const int r = ((f.tile * sub + fs) << res_shift) + row_in_stage(sr);
-            const uint8_t* W = M == kGateUp && (sr & 8) ? p.W2 : p.W;
-            uint32_t n = 0;
-            int64_t from = 0;
-            if (r < p.rows) {
-                const int64_t row = static_cast<int64_t>(expert_of(f.gi)) * p.rows + r;
-                const int64_t start = row * p.row_bytes + fc * p.kc * kBB;
-                from = start & ~static_cast<int64_t>(15);
-                int64_t to = (start + min(p.kc, p.kb - fc * p.kc) * kBB + 15) & ~static_cast<int64_t>(15);
-                if (to > p.total_bytes) {   // the matrix ends inside its last 16-byte word
-                    to = p.total_bytes & ~static_cast<int64_t>(15);
-                    for (int64_t k = to > from ? to : from; k < p.total_bytes; ++k)
-                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(k - from)),
-                                     "r"(static_cast<uint32_t>(W[k])) : "memory");
+    // Starts the copies of the next chunk (if any), as one group. Staged row 8 j + g
+    // (g = lane / 4) is row 8 j + g of the warp's 32 (kGateUp: of the 16 gate rows, then of the
+    // up rows of the same numbers). Whole words from the one that holds the chunk's first byte;
+    // what they hold behind the chunk is not used.
+    __device__ __forceinline__ void issue() {
+        if (fleft > 0) {
+            const int l = lane & 3;
+            const int64_t chunk = frow * p.row_bytes + fc * (kCB * kBB);
+            const uint32_t dst = ring + fstage * kStageBytes + (lane >> 2) * kPitch + 16 * l;
+            if (ftile * 32 + 32 <= p.rows && chunk + 31 * p.row_bytes + 16 * kWords <= p.total_bytes) {
+                int64_t at = chunk + (lane >> 2) * p.row_bytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (M == kGateUp && j == 2) at -= 16 * p.row_bytes;
+                    const uint8_t* from = (M == kGateUp && j >= 2 ? p.W2 : p.W) + ((at & ~int64_t(15)) + 16 * l);
+                    copy16(dst + j * 8 * kPitch, from);
+                    copy16(dst + j * 8 * kPitch + 64, from + 64);
+                    if (l < kWords - 8) copy16(dst + j * 8 * kPitch + 128, from + 128);
+                    at += 8 * p.row_bytes;
                 }
-                if (to > from) n = static_cast<uint32_t>(to - from);
+            } else {
+                issue_last(chunk, dst, l);
             }
-            // the stage's plain reads, before the barrier that brought us here, come first
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive_expect_tx(bar, n);
-            if (n > 0) bulk_g2s_evict_first(dst, W + from, n, bar);
+            fc += kwarps;
+            if (fc >= p.chunks) {
+                fc = wk;
+                if (++fs == kSub) {
+                    fs = 0;
+                    --fleft;
+                    if (++ftile == p.tiles) {
+                        ftile = 0;
+                        ++fgi;
+                    }
+                }
+                if (fleft > 0) copy_row();
+            }
         }
-        if (++fslot == p.stages) fslot = 0;
-        if (++fc == p.chunks) {
-            fc = 0;
-            if (++fs == sub) {
-                fs = 0;
-                f.next(p.units);
-            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        fstage ^= 1;
+    }
+
+    // The same where rows are missing or the buffer ends: no byte past either is read.
+    __device__ __forceinline__ void issue_last(int64_t chunk, uint32_t dst, int l) const {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const int r = (M == kGateUp ? j & 1 : j) * 8 + (lane >> 2);
+            const int64_t from = (chunk + r * p.row_bytes) & ~static_cast<int64_t>(15);
+            const int left = ftile * 32 + fs * 16 + r < p.rows
+                                 ? static_cast<int>(min(p.total_bytes - from, static_cast<int64_t>(16 * kWords))) : 0;
+            const uint8_t* src = (M == kGateUp && j >= 2 ? p.W2 : p.W) + from;
+#pragma unroll 1
+            for (int i = l; 16 * i < left; i += 4)
+                copy16(dst + j * 8 * kPitch + 16 * (i - l), src + 16 * i, min(16, left - 16 * i));
         }
     }
 
-    // Waits for the stage at hand. After a wait that ran out, and an equal one for the other
-    // stages that are under way, goes on without waiting: the results are lost.
-    __device__ __forceinline__ void wait_stage(int slot, uint32_t phase) {
-        if (dead || __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * slot, phase))) return;
-        dead = true;
-        report_status(p.status, kStatusTimeout);
-        for (int i = 1; i < p.stages; ++i) {
-            if (++slot == p.stages) {
-                slot = 0;
-                phase ^= 1;
-            }
-            mbar_wait(full + 8 * slot, phase);
-        }
-    }
-
-    // ---- products ----
-
-    template <int NT>
+    // A unit's activations: where this lane's next block is, moved on with every load.
     struct Acts {
-        Columns<NT, Terms> col[kMaxBlocks];
+        const uint4* b[NT];
+        const float* s[NT][2];
+        const float* sum[NT][2];
     };
 
-    // This lane's share of nb blocks from block kb0 of the group's activations. Columns of
-    // tokens that the group does not have read token 0's: nothing uses them.
-    template <int NT>
-    __device__ __forceinline__ void load_acts(Acts<NT>& a, int gi, int n_tok, int kb0, int nb) const {
-        const int g = lane >> 2, t = lane & 3;
+    // The block at hand, and on to the one `step` blocks later.
+    __device__ __forceinline__ void load(Cols& c, Acts& a, int step) const {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int i = Terms == 2 ? 4 * n + (g >> 1) : 8 * n + g;
-            const int64_t row = x_row(gi, i < n_tok ? i : 0) * Terms + (Terms == 2 ? g & 1 : 0);
-            const uint4* xp = p.xb + (row * p.kb + kb0) * 4 + t;
-#pragma unroll
-            for (int b = 0; b < kMaxBlocks; ++b)
-                if (b < nb) a.col[b].b[n] = xp[b * 4];
-            if constexpr (Terms == 2) {
-                const int j = 4 * n + t;
-                const float2* mp = reinterpret_cast<const float2*>(p.xm) + x_row(gi, j < n_tok ? j : 0) * p.kb + kb0;
-#pragma unroll
-                for (int b = 0; b < kMaxBlocks; ++b)
-                    if (b < nb) a.col[b].m[n] = mp[b];
-            } else {
-                const int j0 = 8 * n + 2 * t;
-                const float* m0 = p.xm + x_row(gi, j0 < n_tok ? j0 : 0) * p.kb + kb0;
-                const float* m1 = p.xm + x_row(gi, j0 + 1 < n_tok ? j0 + 1 : 0) * p.kb + kb0;
-#pragma unroll
-                for (int b = 0; b < kMaxBlocks; ++b)
-                    if (b < nb) a.col[b].m[n] = make_float2(m0[b], m1[b]);
+            if constexpr (Terms == 2)
+                load32(c.b[n], a.b[n]);
+            else
+                c.b[n][0] = *a.b[n];
+            a.b[n] += step * 4 * Terms;
+            if constexpr (kScaled) {
+                c.s[n] = make_float2(*a.s[n][0], *a.s[n][1]);
+                a.s[n][0] += step;
+                a.s[n][1] += step;
+            }
+            if constexpr (kSums) {
+                c.sum[n] = make_float2(*a.sum[n][0], *a.sum[n][1]);
+                a.sum[n][0] += step;
+                a.sum[n][1] += step;
             }
         }
     }
 
-    // nb blocks, from block kb0 of the row (kq0 of the chunk), of this warp's rows of a stage.
-    template <int NT>
-    __device__ __forceinline__ void products(float (&tot)[kTiles][NT][2][3 - Terms], const Acts<NT>& a,
-                                             uint32_t stage, uint32_t row0, int c, int kq0, int nb) const {
-        const int g = lane >> 2, t = lane & 3;
-        const int wr = warp / p.kwarps;
-        // Where this lane's rows begin: the staged word's offset (0..15) of their chunk. Rows g
-        // and g + 8 of every tile agree in the low two bits, as eight rows are a multiple of 8
-        // bytes.
-        uint32_t base[kTiles][2];
+    // One block of the 32 staged rows, whose first byte lies `pos` bytes into every row.
+    __device__ __forceinline__ void block(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int pos,
+                                          const Cols& col) const {
+        // Rows agree in the low two bits of their places (eight rows are a multiple of 8 bytes):
+        // the aligned word before a code word, and the shift that takes the word out of two.
+        constexpr int kHead = T == GQ_TYPE_MXFP4 ? 1 : 2;
+        const uint32_t r = (base[0][0] + pos + kHead) & 3u;
+        const int off = pos + kHead - static_cast<int>(r) + 4 * (lane & 3);
 #pragma unroll
-        for (int ti = 0; ti < kTiles; ++ti)
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t q[2][4];
+            float d[2], m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int sr = (wr * kTiles + ti) * 16 + 8 * h + g;
-                const uint32_t mis = ((row0 + row_in_stage(sr)) * static_cast<uint32_t>(p.row_bytes) +
-                                      static_cast<uint32_t>(c * p.kc) * kBB) & 15u;
-                base[ti][h] = stage + sr * p.pitch + mis;
-            }
-        if constexpr (T == GQ_TYPE_Q4_K) {
-            // four (or two) sub-blocks of one super-block
-            const int in = (kq0 & 7) >> 1;
-#pragma unroll
-            for (int ti = 0; ti < kTiles; ++ti) {
-                uint4 hd[2];
-                float D[2], Dm[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    base[ti][h] += (kq0 >> 3) * kQ4KBytes;
-                    hd[h] = lds128(base[ti][h]);
-                    base[ti][h] += 16 + 32 * in + 4 * t;
-                    D[h] = half_bits_to_float(hd[h].x);
-                    Dm[h] = half_bits_to_float(hd[h].x >> 16);
+                const uint32_t at = base[mt][h] + off;
+                const uint32_t w0 = __funnelshift_r(lds32(at), lds32(at + 4), r << 3);
+                if constexpr (T == GQ_TYPE_Q8_0) {
+                    const uint32_t w1 = __funnelshift_r(lds32(at + 16), lds32(at + 20), r << 3);
+                    const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
+                    // 1024 + 128 + code, byte by byte under the exponent
+                    q[h][0] = h2_sub(__byte_perm(u0, 0x64u, 0x4140), 0x64806480u);
+                    q[h][1] = h2_sub(__byte_perm(u0, 0x64u, 0x4342), 0x64806480u);
+                    q[h][2] = h2_sub(__byte_perm(u1, 0x64u, 0x4140), 0x64806480u);
+                    q[h][3] = h2_sub(__byte_perm(u1, 0x64u, 0x4342), 0x64806480u);
+                } else if constexpr (T == GQ_TYPE_Q4_0) {
+                    nibbles_to_f16<8>(w0, q[h]);
+                } else {
+                    e2m1_to_f16(w0, q[h]);
                 }
+                if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(lds16(base[mt][h] + pos));
+            }
+            if constexpr (T == GQ_TYPE_MXFP4)
+                e8m0_to_f32(lds8(base[mt][0] + pos), lds8(base[mt][1] + pos), d[0], d[1]);
+            block_products<T, Terms, NT, kScaled>(q, d, m, col, tot[mt]);
+        }
+    }
+
+    // Q4_K: sub-blocks 2 j and 2 j + 1, which share code bytes, s = 0 or 1 of them.
+    __device__ __forceinline__ void block_q4k(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int j, int s,
+                                              const Cols& col) const {
 #pragma unroll
-                for (int b = 0; b < kMaxBlocks; b += 2) {
-                    if (b >= nb) break;
-                    uint32_t w[2][2], sc[2], mn[2];
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t q[2][4];
+            float d[2], m[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 hd = lds128(base[mt][h]);
+                const uint32_t at = base[mt][h] + 16 + 32 * j + 4 * (lane & 3);
+                const uint32_t w0 = lds32(at), w1 = lds32(at + 16);
+                const uint32_t mask = s ? 0x00F000F0u : 0x000F000Fu;
+                q[h][0] = (w0 & mask) | kMagic;
+                q[h][1] = ((w0 >> 8) & mask) | kMagic;
+                q[h][2] = (w1 & mask) | kMagic;
+                q[h][3] = ((w1 >> 8) & mask) | kMagic;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[h][i] = s ? h2_fma(q[h][i], kSixteenth, 0xD400D400u) : h2_sub(q[h][i], kMagic);
+                uint32_t sc, mn;
+                q4k_scales(hd, j, sc, mn);
+                d[h] = half_bits_to_float(hd.x) * byte_to_float(sc, s);
+                m[h] = half_bits_to_float(hd.x >> 16) * byte_to_float(mn, s);
+            }
+            block_products<T, Terms, NT, kScaled>(q, d, m, col, tot[mt]);
+        }
+    }
+
+    __device__ __forceinline__ void unit(int gi, int tile, int& stage) {
+        const int n_tok = count_of(gi);
+        const int g = lane >> 2, t = lane & 3;
+        const uint32_t e_row = static_cast<uint32_t>(expert_of(gi)) * static_cast<uint32_t>(p.rows) + tile * 32;
+        float hidden[NT][2][4];   // kGateUp: tokens 2t, 2t + 1 x rows g, 8 + g of either pass
+#pragma unroll 1
+        for (int s = 0; s < kSub; ++s) {
+            // Columns of tokens that the group does not have read token 0's: nothing uses them.
+            // Loads run ahead, past a row's end by up to kAhead blocks: the workspace goes on.
+            Acts acts;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acts.b[n] = p.xb + (static_cast<int64_t>(x_row(gi, 8 * n + g < n_tok ? 8 * n + g : 0)) * p.kb + wk * kCB) * 4 * Terms + t * Terms;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = 8 * n + 2 * t + i;
+                    const int64_t at = static_cast<int64_t>(x_row(gi, tok < n_tok ? tok : 0)) * p.kb + wk * kCB;
+                    if constexpr (kScaled) acts.s[n][i] = p.xs + at;
+                    if constexpr (kSums) acts.sum[n][i] = p.xsum + at;
+                }
+            }
+            float tot[2][NT][4];
+#pragma unroll
+            for (int i = 0; i < kTotals; ++i) (&tot[0][0][0])[i] = 0.0f;
+            Cols col[2];
+            const int jump = (kwarps - 1) * kCB + 1;   // from a chunk's last block to the next's first
+            load(col[0], acts, 1);
+            load(col[1], acts, kCB > 2 ? 1 : jump);
+#pragma unroll 1
+            for (int c = wk; c < p.chunks; c += kwarps) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+                __syncwarp();
+                const int nb = min(kCB, p.kb - c * kCB);
+                // Where this lane's rows begin inside their staged words (0..15).
+                uint32_t base[2][2];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        w[h][0] = lds32(base[ti][h] + 16 * b);
-                        w[h][1] = lds32(base[ti][h] + 16 + 16 * b);
-                        q4k_scales(hd[h], in + (b >> 1), sc[h], mn[h]);
+                        const uint32_t row = e_row + (M == kGateUp ? 16 * s + 8 * h + g : 16 * mt + 8 * h + g);
+                        base[mt][h] = ring + stage * kStageBytes + (16 * mt + 8 * h + g) * kPitch +
+                                      ((row * static_cast<uint32_t>(p.row_bytes) + static_cast<uint32_t>(c) * (kCB * kBB)) & 15u);
                     }
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        uint32_t q[2][4];
-                        float d[2], m[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t mask = s ? 0x00F000F0u : 0x000F000Fu;
-                            q[h][0] = (w[h][0] & mask) | kMagic;
-                            q[h][1] = ((w[h][0] >> 8) & mask) | kMagic;
-                            q[h][2] = (w[h][1] & mask) | kMagic;
-                            q[h][3] = ((w[h][1] >> 8) & mask) | kMagic;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                q[h][i] = s ? h2_fma(q[h][i], kSixteenth, 0xD400D400u)
-                                            : h2_sub(q[h][i], kMagic);
-                            d[h] = D[h] * byte_to_float(sc[h], s);
-                            m[h] = Dm[h] * byte_to_float(mn[h], s);
-                        }
-                        block_products<T, Terms, NT>(q, d, m, a.col[b + s], tot[ti]);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int ti = 0; ti < kTiles; ++ti)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) base[ti][h] += kq0 * kBB;
-            // Unaligned words: the aligned word at (base + delta[j] + 4-multiple) and its
-            // successor, shifted by shift[j], for byte offsets congruent j modulo 4.
-            const uint32_t r3 = base[0][0] & 3u;
-            int delta[4];
-            uint32_t shift[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                delta[j] = (r3 + j >= 4 ? 4 : 0) - static_cast<int>(r3) + 4 * t;
-                shift[j] = (r3 + j) << 3;   // the funnel shift takes it modulo 32
-            }
-#pragma unroll
-            for (int b = 0; b < kMaxBlocks; ++b) {
-                if (b >= nb) break;
-#pragma unroll
-                for (int ti = 0; ti < kTiles; ++ti) {
-                    uint32_t q[2][4];
-                    float d[2], m[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        constexpr int kHead = T == GQ_TYPE_MXFP4 ? 1 : 2;
-                        const int off = b * kBB + kHead;
-                        const uint32_t at = base[ti][h] + delta[off & 3] + (off & ~3);
-                        const uint32_t w0 = __funnelshift_r(lds32(at), lds32(at + 4), shift[off & 3]);
-                        if constexpr (T == GQ_TYPE_Q8_0) {
-                            const uint32_t w1 = __funnelshift_r(lds32(at + 16), lds32(at + 20), shift[off & 3]);
-                            const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
-                            // 1024 + 128 + code, byte by byte under the exponent
-                            q[h][0] = h2_sub(__byte_perm(u0, 0x64u, 0x4140), 0x64806480u);
-                            q[h][1] = h2_sub(__byte_perm(u0, 0x64u, 0x4342), 0x64806480u);
-                            q[h][2] = h2_sub(__byte_perm(u1, 0x64u, 0x4140), 0x64806480u);
-                            q[h][3] = h2_sub(__byte_perm(u1, 0x64u, 0x4342), 0x64806480u);
-                        } else if constexpr (T == GQ_TYPE_Q4_0) {
-                            nibbles_to_f16<8>(w0, q[h]);
-                        } else {
-                            e2m1_to_f16(w0, q[h]);
-                        }
-                        if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(lds16(base[ti][h] + b * kBB));
-                    }
-                    if constexpr (T == GQ_TYPE_MXFP4)
-                        e8m0_to_f32(lds8(base[ti][0] + b * kBB), lds8(base[ti][1] + b * kBB), d[0], d[1]);
-                    block_products<T, Terms, NT>(q, d, m, a.col[b], tot[ti]);
-                }
-            }
-        }
-    }
-
-    // The units of this CTA from `at` on whose groups have as many tokens as NT column tiles are
-    // for.
-    template <int NT>
-    __device__ __forceinline__ void consume(Place& at, int& slot, uint32_t& phase) {
-        constexpr int kTile = 4 * (3 - Terms);
-        constexpr int kPitch = NT * kTile + 1;   // of a row of sums
-        const int wk = warp & (p.kwarps - 1);
-        const int kq0 = wk * p.per;
-        Acts<NT> acts;
-        int held = -1, side = 0;
-        __syncthreads();   // the sums are free
+                // pairs of blocks; a column set is loaded again as soon as it has been used
 #pragma unroll 1
-        for (; at.left > 0; at.next(p.units)) {
-            const int n_tok = count_of(at.gi);
-            if (n_tok > NT * kTile || n_tok <= (NT - 1) * kTile) break;
-            const uint32_t e_row = static_cast<uint32_t>(expert_of(at.gi)) * static_cast<uint32_t>(p.rows);
-#pragma unroll 1
-            for (int s = 0; s < sub; ++s) {
-                float tot[kTiles][NT][2][3 - Terms];
-#pragma unroll
-                for (int i = 0; i < kTiles * NT * 2 * (3 - Terms); ++i) (&tot[0][0][0][0])[i] = 0.0f;
-                const int row0 = first_row(at.tile, s);
-#pragma unroll 1
-                for (int c = 0; c < p.chunks; ++c) {
-                    const int nb = min(p.per, min(p.kc, p.kb - c * p.kc) - kq0);
-                    if (held != at.gi || p.chunks > 1) {
-                        load_acts<NT>(acts, at.gi, n_tok, c * p.kc + kq0, nb);
-                        held = at.gi;
-                    }
-                    wait_stage(slot, phase);
-                    if (nb > 0) products<NT>(tot, acts, ring + slot * p.stage_bytes, e_row + row0, c, kq0, nb);
-                    if (++slot == p.stages) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
-                    if (c + 1 < p.chunks) {   // after the last chunk, the join's barrier does this
-                        __syncthreads();
-                        if (!dead) fill();
-                    }
+                for (int b = 0; b + 1 < nb; b += 2) {
+                    const int step = b + 4 == nb ? jump : 1;   // block b + 3 ends the chunk
+                    if constexpr (T == GQ_TYPE_Q4_K)
+                        block_q4k(tot, base, b >> 1, 0, col[0]);
+                    else
+                        block(tot, base, b * kBB, col[0]);
+                    load(col[0], acts, 1);
+                    if constexpr (T == GQ_TYPE_Q4_K)
+                        block_q4k(tot, base, b >> 1, 1, col[1]);
+                    else
+                        block(tot, base, (b + 1) * kBB, col[1]);
+                    load(col[1], acts, step);
                 }
-                // Two halves of the sums in turn: one barrier is enough.
-                float* const half = sums + (side ? kSumFloats / 2 : 0);
-                side ^= 1;
-                float* mine = half + (warp * kTiles * 16 + (lane >> 2)) * kPitch;
-#pragma unroll
-                for (int ti = 0; ti < kTiles; ++ti)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int i = 0; i < 3 - Terms; ++i) {
-                                const int tok = Terms == 2 ? 4 * n + (lane & 3) : 8 * n + 2 * (lane & 3) + i;
-                                mine[(16 * ti + 8 * h) * kPitch + tok] = tot[ti][n][h][i];
-                            }
-                __syncthreads();
-                if (!dead) fill();
-                finish<kPitch>(half, at.gi, n_tok, s, row0);
+                if constexpr (T != GQ_TYPE_Q4_K)
+                    if (nb & 1) block(tot, base, (nb - 1) * kBB, col[0]);   // only a row's last chunk
+                __syncwarp();   // every lane has read its part of the stage
+                issue();
+                stage ^= 1;
             }
-            if constexpr (M == kGateUp) split_hidden(at.gi, n_tok, at.tile);
-        }
-    }
-
-    // Staged row sr, token i: the K warps' sums in their order.
-    template <int Pitch>
-    __device__ __forceinline__ float joined(const float* at, int sr, int i) const {
-        constexpr int kRows = 16 * kTiles;
-        const float* from = at + ((sr / kRows) * p.kwarps * kRows + sr % kRows) * Pitch + i;
-        float v = 0.0f;
-        for (int k = 0; k < p.kwarps; k += 4) {   // 4, 8 or 16 of them
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = from[(k + j) * kRows * Pitch];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v += x[j];
-        }
-        return v;
-    }
-
-    template <int Pitch>
-    __device__ __forceinline__ void finish(const float* at, int gi, int n_tok, int s, int row0) const {
-        for (int i = threadIdx.x; i < (n_tok << res_shift); i += kThreads) {
-            const int r = i & ((1 << res_shift) - 1), tok = i >> res_shift;
+            if (kwarps > 1) join(&tot[0][0][0]);
             if constexpr (M == kGateUp) {
-                const int sr = (r >> 3) * 16 + (r & 7);
-                const float gate = joined<Pitch>(at, sr, tok), up = joined<Pitch>(at, sr + 8, tok);
-                hidden[((s << res_shift) + r) * (kFewGroup + 1) + tok] = gate / (1.0f + expf(-gate)) * up;
-            } else if (row0 + r < p.rows) {
-                float* const out = M == kDown ? p.part : p.Y;
-                out[x_row(gi, tok) * p.rows + row0 + r] = joined<Pitch>(at, r, tok);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 8 * n + 2 * t + (i & 1);
+                        const float sc = p.xs[x_row(gi, tok < n_tok ? tok : 0)];
+                        const float gate = tot[0][n][i] * sc, v = gate / (1.0f + expf(-gate)) * (tot[1][n][i] * sc);
+                        if (s == 0) hidden[n][i & 1][i >> 1] = v;
+                        else hidden[n][i & 1][2 + (i >> 1)] = v;
+                    }
+            } else if (wk == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = 8 * n + 2 * t + i;
+                        if (tok < n_tok) {
+                            const int64_t row = x_row(gi, tok);
+                            const float sc = kScaled ? 1.0f : p.xs[row];
+                            float* out = p.out + row * p.rows + tile * 32 + g;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)   // rows 8 k + g
+                                if (tile * 32 + 8 * k + g < p.rows) out[8 * k] = tot[k >> 1][n][2 * (k & 1) + i] * sc;
+                        }
+                    }
             }
+        }
+        if constexpr (M == kGateUp)
+            if (wk == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (8 * n < n_tok) write_hidden(gi, tile, 8 * n + 2 * t + i, n_tok, hidden[n][i]);
+            }
+    }
+
+    // The split activations of token `tok`'s 32 hidden values of a unit; this lane has elements
+    // g, 8 + g, 16 + g and 24 + g.
+    __device__ __forceinline__ void write_hidden(int gi, int tile, int tok, int n_tok, const float (&h)[4]) const {
+        const int g = lane >> 2;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const int e = block_exponent(amax);
+        const int64_t at = static_cast<int64_t>(tok < n_tok ? L.pair[L.start[gi] + tok] : 0) * (p.rows / 32) + tile;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Split s(h[i], e);
+            sum += s.sum();
+            if (tok < n_tok) {
+                const int place = few_place(p.h_type, 8 * i + g);
+                __half* out = p.hb + at * 64 + place + (place & ~7);   // hi and lo by eights
+                out[0] = s.hi;
+                out[8] = s.lo;
+            }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (g == 0 && tok < n_tok) {
+            p.hs[at] = pow2f(e - 14);
+            p.hsum[at] = pow2f(e - 14) * sum;
         }
     }
 
-    // kGateUp: the unit's hidden values to split activations, one warp per (block, token).
-    __device__ __forceinline__ void split_hidden(int gi, int n_tok, int tile) const {
-        __syncthreads();
-        const int blocks = (sub << res_shift) / 32;   // 1 or 2
-        const int hb = p.rows / 32;
-        const int place = few_place(p.h_type, lane);
-        for (int i = warp; i < blocks * n_tok; i += kWarps) {
-            const int bl = i & (blocks - 1), tok = i / blocks;
-            const int blk = tile * blocks + bl;
-            if (blk >= hb) continue;
-            const int64_t q = L.pair[L.start[gi] + tok];
-            write_split(hidden[(32 * bl + lane) * (kFewGroup + 1) + tok], lane, place,
-                        p.hb + (q * 2 * hb + blk) * 32, hb * 32, p.hm + q * hb + blk);
+    // Adds the K warps' totals, in their order, into the first one's.
+    __device__ __forceinline__ void join(float* tot) {
+        float* const at = sums + wr * kwarps * kTotals * 32 + lane;
+        if (wk > 0) {
+#pragma unroll
+            for (int i = 0; i < kTotals; ++i) at[(wk * kTotals + i) * 32] = tot[i];
         }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * kwarps) : "memory");
+        if (wk == 0) {
+#pragma unroll 1
+            for (int k = 1; k < kwarps; ++k)
+#pragma unroll
+                for (int i = 0; i < kTotals; ++i) tot[i] += at[(k * kTotals + i) * 32];
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * kwarps) : "memory");
     }
 };
 
-template <int T, int M, int Terms>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Params p) {
+template <int T, int M, int Terms, int NT>
+__global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ Params p) {
+    using Wk = Worker<T, M, Terms, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[kMaxStages];
-    Lists& L = *reinterpret_cast<Lists*>(smem);
-    float* const sums = reinterpret_cast<float*>(smem + kListBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Lists& L = *reinterpret_cast<Lists*>(smem + Wk::kRingBytes + Wk::kSumBytes);
+    const int warp = threadIdx.x >> 5;
     griddep_launch_dependents();
-    Worker<T, M, Terms> w{p, L, sums, sums + kSumFloats, smem_addr(smem) + kRingAt, smem_addr(bars), lane, warp};
-    w.stage_rows = 16 * Fmt<T>::tiles * (kWarps / p.kwarps);
-    if (threadIdx.x < p.stages) mbar_init(smem_addr(&bars[threadIdx.x]), w.stage_rows);
-    if (threadIdx.x == 0) fence_mbar_init();
-    if (M != kDense) build_lists(p, L, reinterpret_cast<int*>(sums));
-    __syncthreads();
-    w.res_shift = 31 - __clz(M == kGateUp ? w.stage_rows / 2 : w.stage_rows);
-    w.sub = M == kGateUp ? max(1, 32 >> w.res_shift) : 1;
-    w.groups = M == kDense ? static_cast<int>((p.N + kFewGroup - 1) / kFewGroup) : L.groups;
-    // consecutive units for each CTA: those of one group follow each other
-    const int64_t total = static_cast<int64_t>(w.groups) * p.units;
-    const int64_t begin = total * blockIdx.x / gridDim.x;
-    Place at{static_cast<int>(begin / p.units), static_cast<int>(begin % p.units),
-             total * (blockIdx.x + 1) / gridDim.x - begin};
-    w.f = at;
-    w.fs = w.fc = w.fslot = 0;
-    w.dead = false;
+    if (M != kDense) build_lists(p.ids, p.E, p.top_k, p.pairs, Wk::kGroup, L, reinterpret_cast<int*>(smem));
+    Wk w{p, L, smem_addr(smem) + warp * kStages * Wk::kStageBytes, reinterpret_cast<float*>(smem + Wk::kRingBytes)};
+    w.lane = threadIdx.x & 31;
+    w.kwarps = 1 << p.kshift;
+    w.wk = warp & (w.kwarps - 1);
+    w.wr = warp >> p.kshift;
+    const int groups = M == kDense ? (p.N + Wk::kGroup - 1) / Wk::kGroup : L.groups;
+    // consecutive units for each row warp; the host keeps their number below 2^30
+    const int rwarps = kWarps >> p.kshift;
+    const int64_t units = static_cast<int64_t>(groups) * p.tiles;
+    const int row_warp = blockIdx.x * rwarps + w.wr, row_warps = gridDim.x * rwarps;
+    const int begin = static_cast<int>(units * row_warp / row_warps);
+    int left = static_cast<int>(units * (row_warp + 1) / row_warps) - begin;
+    int gi = begin / p.tiles, tile = begin - gi * p.tiles;
+    w.fgi = gi;
+    w.ftile = tile;
+    w.fleft = left;
+    w.fs = w.fstage = 0;
+    w.fc = w.wk;
+    if (left > 0) w.copy_row();
 #pragma unroll 1
-    for (int i = 0; i < p.stages; ++i) w.fill();
-    griddep_wait();   // activations (and what this kernel writes) belong to the kernels before
-    int slot = 0;
-    uint32_t phase = 0;
+    for (int i = 0; i < kStages; ++i) w.issue();
+    griddep_wait();   // activations, and what this kernel writes, belong to the kernels before
+    int stage = 0;
 #pragma unroll 1
-    while (at.left > 0) {
-        if (w.count_of(at.gi) <= 4 * (3 - Terms)) {
-            w.template consume<1>(at, slot, phase);
-        } else {
-            if constexpr (Terms == 2) w.template consume<2>(at, slot, phase);
+    for (; left > 0; --left) {
+        w.unit(gi, tile, stage);
+        if (++tile == p.tiles) {
+            tile = 0;
+            ++gi;
         }
     }
 }
 
 // Y[n] = sum_j weights[n][j] part[n][j], over the pairs that have an expert, in the order of j.
+// One CTA row per token.
 __global__ void __launch_bounds__(256)
 combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
-               const float* __restrict__ weights, int64_t N, int top_k, int E, int D,
-               float* __restrict__ Y) {
+               const float* __restrict__ weights, int top_k, int E, int D, float* __restrict__ Y) {
     griddep_wait();   // `part`, and Y, which the kernels before may still read as X
-    const int quads = D / 4;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < N * quads; i += step) {
-        const int64_t n = i / quads;
-        const int r = static_cast<int>(i - n * quads);
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int j = 0; j < top_k; ++j) {
-            const int64_t q = n * top_k + j;
-            const int id = ids[q];
-            if (id < 0 || id >= E) continue;
-            const float w = weights[q];
-            const float4 v = reinterpret_cast<const float4*>(part)[q * quads + r];
-            y.x = fmaf(w, v.x, y.x);
-            y.y = fmaf(w, v.y, y.y);
-            y.z = fmaf(w, v.z, y.z);
-            y.w = fmaf(w, v.w, y.w);
-        }
-        float* out = Y + n * D + 4 * r;   // only 4-byte aligned
-        out[0] = y.x;
-        out[1] = y.y;
-        out[2] = y.z;
-        out[3] = y.w;
+    const int n = blockIdx.y, quads = D / 4;
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    if (r >= quads) return;
+    const float4* const from = reinterpret_cast<const float4*>(part) + static_cast<int64_t>(n) * top_k * quads + r;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int j = 0; j < top_k; ++j) {
+        const int id = ids[n * top_k + j];
+        if (id < 0 || id >= E) continue;
+        const float w = weights[n * top_k + j];
+        const float4 v = from[static_cast<int64_t>(j) * quads];
+        y.x = fmaf(w, v.x, y.x);
+        y.y = fmaf(w, v.y, y.y);
+        y.z = fmaf(w, v.z, y.z);
+        y.w = fmaf(w, v.w, y.w);
     }
+    float* out = Y + static_cast<int64_t>(n) * D + 4 * r;   // only 4-byte aligned
+    out[0] = y.x;
+    out[1] = y.y;
+    out[2] = y.z;
+    out[3] = y.w;
 }
 
 // ---- Preparation ------------------------------------------------------------------------
 
-// One warp per 32-element block of X: two-term split activations in the order of `type`.
-__global__ void __launch_bounds__(256)
-split_kernel(const float* __restrict__ X, int64_t n_blocks, int kb, int type,
-             __half* __restrict__ xb, float2* __restrict__ xm) {
+// One CTA per row of X: two-term split activations in the order of `type`, one scale for the
+// row; for Q4_K the sums of its blocks in scaled units.
+__global__ void __launch_bounds__(512)
+split_kernel(const float* __restrict__ X, int kb, int type, __half* __restrict__ xb, float* __restrict__ xs,
+             float* __restrict__ xsum) {
+    __shared__ uint32_t most[16];
     griddep_launch_dependents();
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
+    const float* x = X + row * kb * 32;
+    uint32_t amax = 0;
+#pragma unroll 4
+    for (int b = warp; b < kb; b += 16) amax = max(amax, __float_as_uint(x[b * 32 + lane]) & 0x7FFFFFFFu);
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    if (lane == 0) most[warp] = amax;
+    __syncthreads();
+    const int e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, most[lane & 15]));
+    if (threadIdx.x == 0) xs[row] = pow2f(e - 14);
     const int place = few_place(type, lane);
-    for (int64_t b = warp; b < n_blocks; b += step) {
-        const int64_t row = b / kb, blk = b % kb;
-        write_split(X[b * 32 + lane], lane, place, xb + (row * 2 * kb + blk) * 32,
-                    static_cast<int64_t>(kb) * 32, xm + b);
+    __half* out = xb + row * kb * 64 + place + (place & ~7);   // hi and lo by eights
+#pragma unroll 4
+    for (int b = warp; b < kb; b += 16) {
+        const Split s(x[b * 32 + lane], e);
+        out[b * 64] = s.hi;
+        out[b * 64 + 8] = s.lo;
+        if (type == GQ_TYPE_Q4_K) {
+            float sum = s.sum();
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if (lane == 0) xsum[row * kb + b] = sum;
+        }
     }
 }
 
-// One warp per block: X quantized to MXFP4, kept as fp16 values and one scale.
+// One warp per block (blockIdx.y: the row): X quantized to MXFP4, kept as fp16 values and one
+// scale.
 __global__ void __launch_bounds__(256)
-mx_split_kernel(const float* __restrict__ X, int64_t n_blocks, __half* __restrict__ xb,
-                float* __restrict__ xm) {
+mx_split_kernel(const float* __restrict__ X, int kb, __half* __restrict__ xb, float* __restrict__ xm) {
     griddep_launch_dependents();
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int place = few_place(GQ_TYPE_MXFP4, lane);
-    for (int64_t b = warp; b < n_blocks; b += step) {
-        const float x = X[b * 32 + lane];
-        const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
-        const uint32_t byte = mx_scale_byte(amax);
-        uint32_t m = 0;
-        if (byte != 255) m = e2m1_code(fabsf(x) * mx_inverse_scale(byte));
-        const float mag = m < 4 ? 0.5f * static_cast<float>(m)
-                                : static_cast<float>(m < 6 ? m - 2 : 2 * m - 8);
-        xb[b * 32 + place] = __float2half_rn(copysignf(mag, x));
-        if (lane == 0) xm[b] = mx_scale(byte);
-    }
+    const int blk = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (blk >= kb) return;
+    const int64_t b = static_cast<int64_t>(blockIdx.y) * kb + blk;
+    const float x = X[b * 32 + lane];
+    const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu));
+    uint32_t m = 0;
+    if (byte != 255) m = e2m1_code(fabsf(x) * mx_inverse_scale(byte));
+    const float mag = m < 4 ? 0.5f * static_cast<float>(m)
+                            : static_cast<float>(m < 6 ? m - 2 : 2 * m - 8);
+    xb[b * 32 + few_place(GQ_TYPE_MXFP4, lane)] = __float2half_rn(copysignf(mag, x));
+    if (lane == 0) xm[b] = mx_scale(byte);
 }
 
 // ---- Host side --------------------------------------------------------------------------
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-cudaError_t launch_split(const float* X, int64_t rows, int kb, int type, __half* xb, float2* xm,
-                         const DeviceInfo* info, cudaStream_t s) {
-    const int64_t blocks = rows * kb;
-    const int64_t grid = std::min<int64_t>((blocks + 7) / 8, int64_t(info->sm_count) * 8);
-    split_kernel<<<static_cast<unsigned>(std::max<int64_t>(grid, 1)), 256, 0, s>>>(
-        X, blocks, kb, type, xb, xm);
+// The workspace of split activations of n rows: values (and what loads that run ahead may read
+// behind them), scales (one a row, or one a block), sums.
+constexpr int kAhead = 64;   // blocks: eight warps' chunks of eight
+
+struct SplitSpace {
+    int64_t b, s, sum, bytes;
+};
+
+SplitSpace split_space(int64_t n, int64_t K, int terms, bool sums) {
+    SplitSpace x{};
+    x.s = align256((n * K + kAhead * 32) * 2 * terms);
+    x.sum = x.s + align256((n * (K / 32) + kAhead) * 4);
+    x.bytes = x.sum + (sums ? align256((n * (K / 32) + kAhead) * 4) : 0);
+    return x;
+}
+
+cudaError_t launch_split(const float* X, int64_t rows, int kb, int type, uint8_t* ws, const SplitSpace& at,
+                         cudaStream_t s) {
+    split_kernel<<<static_cast<unsigned>(rows), 512, 0, s>>>(
+        X, kb, type, reinterpret_cast<__half*>(ws + at.b), reinterpret_cast<float*>(ws + at.s),
+        reinterpret_cast<float*>(ws + at.sum));
     return cudaGetLastError();
+}
+
+void use_split(Params& p, const uint8_t* ws, const SplitSpace& at) {
+    p.xb = reinterpret_cast<const uint4*>(ws + at.b);
+    p.xs = reinterpret_cast<const float*>(ws + at.s);
+    p.xsum = reinterpret_cast<const float*>(ws + at.sum);
+}
+
+// log2 of the warps that split a unit's K. Every row warp takes the same number of units but for
+// one; the split that leaves the least idle wins, a join counting as 3 %.
+int pick_kshift(int64_t units, int chunks, int warps) {
+    int best = 0;
+    double most = -1.0;
+    for (int ks = 0; ks <= 3 && (1 << ks) <= chunks; ++ks) {
+        const double rw = warps >> ks, rounds = static_cast<double>((units + (warps >> ks) - 1) / (warps >> ks));
+        const double use = units / (rw * rounds) - 0.03 * ks;
+        if (use > most) {
+            most = use;
+            best = ks;
+        }
+    }
+    return best;
 }
 
 // A launch that may start while the kernel before it on the stream still runs (it waits with
 // griddep_wait).
 template <typename... Sig, typename... Args>
-cudaError_t launch_after(void (*kernel)(Sig...), unsigned grid, int threads, int smem, cudaStream_t s,
+cudaError_t launch_after(void (*kernel)(Sig...), dim3 grid, int threads, int smem, cudaStream_t s,
                          const Args&... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
@@ -831,50 +863,43 @@ cudaError_t launch_after(void (*kernel)(Sig...), unsigned grid, int threads, int
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int T, int M, int Terms>
-cudaError_t launch_few(Params& p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
-    // Chunks of up to 64 blocks (four for each of the 16 consumer warps), of equal size but for
-    // the last; with fewer blocks, fewer warps share a chunk and a stage has more rows.
-    constexpr int kMax = kWarps * kMaxBlocks;
-    constexpr int kUnit = T == GQ_TYPE_Q4_K ? 8 : 1;   // super-blocks stay whole
-    p.chunks = (p.kb + kMax - 1) / kMax;
-    p.kc = ((p.kb + p.chunks - 1) / p.chunks + kUnit - 1) / kUnit * kUnit;
-    p.kwarps = p.kc > kMax / 2 ? kWarps : (p.kc > kMax / 4 ? kWarps / 2 : kWarps / 4);
-    p.per = (p.kc + p.kwarps - 1) / p.kwarps;
-    if (T == GQ_TYPE_Q4_K) p.per = (p.per + 1) / 2 * 2 == 2 ? 2 : 4;   // inside one super-block
-    const int stage_rows = 16 * Fmt<T>::tiles * (kWarps / p.kwarps);
-    const int results = M == kGateUp ? stage_rows / 2 : stage_rows;
-    const int unit_rows = M == kGateUp ? std::max(32, results) : results;
-    p.units = (p.rows + unit_rows - 1) / unit_rows;
-    // A row's words, at an odd multiple of 16 bytes: the eight rows that a warp reads at once
-    // then lie on distinct groups of four banks.
-    p.pitch = (p.kc * Fmt<T>::bb + 15 + 15) / 16 * 16;
-    if (p.pitch % 32 == 0) p.pitch += 16;
-    p.stage_bytes = (stage_rows * p.pitch + 16 + 127) / 128 * 128;   // 16: the last word's second half
-    p.stages = std::min(kMaxStages, (kSmemMax - kRingAt) / p.stage_bytes);
-    p.status = info->status;
+// `groups`: how many there are likely to be.
+template <int T, int M, int Terms, int NT>
+cudaError_t launch_few(Params p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
+    using Wk = Worker<T, M, Terms, NT>;
+    p.chunks = (p.kb + Fmt<T>::cb - 1) / Fmt<T>::cb;
+    p.tiles = (p.rows + 31) / 32;
+    const int64_t units = p.tiles * groups;
+    p.kshift = pick_kshift(units, p.chunks, 2 * info->sm_count * kWarps);
+    const int64_t rwarps = kWarps >> p.kshift;
     const unsigned grid = static_cast<unsigned>(
-        std::max<int64_t>(1, std::min<int64_t>(p.units * groups, info->sm_count)));
-    const int smem = kRingAt + p.stages * p.stage_bytes;
-    auto kernel = few_kernel<T, M, Terms>;
+        std::max<int64_t>(1, std::min<int64_t>((units + rwarps - 1) / rwarps, int64_t(info->sm_count) * 2)));
+    auto kernel = few_kernel<T, M, Terms, NT>;
     static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
     const uint64_t bit = uint64_t(1) << info->device;
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Wk::kSmem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_after(kernel, grid, kThreads, smem, s, static_cast<const Params&>(p));
+    return launch_after(kernel, dim3(grid), kThreads, Wk::kSmem, s, p);
+}
+
+// Two-term launch with one or two tiles of 8 tokens.
+template <int T, int M>
+cudaError_t launch_sized(const Params& p, bool wide, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
+    return wide ? launch_few<T, M, 2, 2>(p, groups, info, s) : launch_few<T, M, 2, 1>(p, groups, info, s);
 }
 
 template <int M>
-cudaError_t launch_typed(gq_type t, Params& p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
+cudaError_t launch_typed(gq_type t, const Params& p, bool wide, int64_t groups, const DeviceInfo* info,
+                         cudaStream_t s) {
     switch (t) {
-        case GQ_TYPE_Q4_0: return launch_few<GQ_TYPE_Q4_0, M, 2>(p, groups, info, s);
-        case GQ_TYPE_Q8_0: return launch_few<GQ_TYPE_Q8_0, M, 2>(p, groups, info, s);
-        case GQ_TYPE_Q4_K: return launch_few<GQ_TYPE_Q4_K, M, 2>(p, groups, info, s);
-        case GQ_TYPE_MXFP4: return launch_few<GQ_TYPE_MXFP4, M, 2>(p, groups, info, s);
+        case GQ_TYPE_Q4_0: return launch_sized<GQ_TYPE_Q4_0, M>(p, wide, groups, info, s);
+        case GQ_TYPE_Q8_0: return launch_sized<GQ_TYPE_Q8_0, M>(p, wide, groups, info, s);
+        case GQ_TYPE_Q4_K: return launch_sized<GQ_TYPE_Q4_K, M>(p, wide, groups, info, s);
+        case GQ_TYPE_MXFP4: return launch_sized<GQ_TYPE_MXFP4, M>(p, wide, groups, info, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -888,23 +913,23 @@ Params dense_params(const MatProblem& m, int64_t n0, int64_t n) {
     p.total_bytes = p.row_bytes * m.M;
     p.rows = static_cast<int>(m.M);
     p.kb = static_cast<int>(m.K / 32);
-    p.N = n;
-    p.Y = m.Y + n0 * m.M;
+    p.N = static_cast<int>(n);
+    p.out = m.Y + n0 * m.M;
     return p;
 }
 
 struct MoeSpace {   // offsets in the workspace of one launch over n tokens
-    int64_t xb, xm, hb, hm, part, bytes;
+    SplitSpace x, h;
+    int64_t h_at, part, bytes;
 };
 
 MoeSpace moe_space(const MoeProblem& m, int64_t n) {
     const int64_t pairs = n * m.top_k;
     MoeSpace s{};
-    s.xb = 0;
-    s.xm = s.xb + align256(n * m.D * 4);
-    s.hb = s.xm + align256(n * (m.D / 32) * 8);
-    s.hm = s.hb + align256(pairs * m.F * 4);
-    s.part = s.hm + align256(pairs * (m.F / 32) * 8);
+    s.x = split_space(n, m.D, 2, true);
+    s.h = split_space(pairs, m.F, 2, true);
+    s.h_at = s.x.bytes;
+    s.part = s.h_at + s.h.bytes;
     s.bytes = s.part + align256(pairs * m.D * 4);
     return s;
 }
@@ -919,14 +944,14 @@ int64_t moe_tokens_per_launch(const MoeProblem& m) {
 
 int64_t few_workspace_bytes(int64_t K, int64_t N) {
     const int64_t n = std::min(N, kFewMaxTokens);
-    return align256(n * K * 4) + align256(n * (K / 32) * 8);
+    return split_space(n, K, 2, false).bytes;
 }
 
 // Tokens of one launch: few enough for the workspace, and for 2^30 units.
 int64_t few_tokens_that_fit(int64_t M, int64_t K, int64_t N, int64_t workspace_bytes) {
-    const int64_t units = std::max<int64_t>(kFewGroup, (int64_t(1) << 30) / ((M + 31) / 32) * kFewGroup);
+    const int64_t units = std::max<int64_t>(16, (int64_t(1) << 30) / ((M + 31) / 32) * 8);
     int64_t n = std::min(std::min(N, kFewMaxTokens), units);
-    while (n > 0 && few_workspace_bytes(K, n) > workspace_bytes) n = n > kFewGroup ? n / 2 : n - 1;
+    while (n > 0 && few_workspace_bytes(K, n) > workspace_bytes) n = n > 16 ? n / 2 : n - 1;
     return n;
 }
 
@@ -941,19 +966,17 @@ cudaError_t launch_few_mul_mat(const MatProblem& m, int64_t N, void* workspace,
     for (int64_t n0 = 0; n0 < N && e == cudaSuccess; n0 += per) {
         const int64_t n = std::min(per, N - n0);
         Params p = dense_params(m, n0, n);
-        float2* xm = reinterpret_cast<float2*>(ws + align256(n * m.K * 4));
-        p.xb = reinterpret_cast<const uint4*>(ws);
-        p.xm = reinterpret_cast<const float*>(xm);
-        e = launch_split(m.X + n0 * m.K, n, p.kb, GQ_TYPE_MXFP4, reinterpret_cast<__half*>(ws), xm,
-                         info, s);
+        const SplitSpace at = split_space(n, m.K, 2, false);
+        use_split(p, ws, at);
+        e = launch_split(m.X + n0 * m.K, n, p.kb, GQ_TYPE_MXFP4, ws, at, s);
         if (e == cudaSuccess)
-            e = launch_few<GQ_TYPE_MXFP4, kDense, 2>(p, (n + kFewGroup - 1) / kFewGroup, info, s);
+            e = launch_sized<GQ_TYPE_MXFP4, kDense>(p, n > 8, n > 8 ? (n + 15) / 16 : 1, info, s);
     }
     return e;
 }
 
 int64_t few_mx_workspace_bytes(int64_t K, int64_t N) {
-    return align256(N * K * 2) + align256(N * (K / 32) * 4);
+    return split_space(N, K, 1, false).bytes;
 }
 
 cudaError_t launch_few_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStream_t s) {
@@ -962,16 +985,15 @@ cudaError_t launch_few_mx4x(const MatProblem& m, int64_t N, void* workspace, cud
     if (e != cudaSuccess) return e;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     Params p = dense_params(m, 0, N);
-    float* xm = reinterpret_cast<float*>(ws + align256(N * m.K * 2));
-    p.xb = reinterpret_cast<const uint4*>(ws);
-    p.xm = xm;
-    const int64_t blocks = N * p.kb;
-    const int64_t grid = std::min<int64_t>((blocks + 7) / 8, int64_t(info->sm_count) * 8);
-    mx_split_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(
-        m.X, blocks, reinterpret_cast<__half*>(ws), xm);
+    const SplitSpace at = split_space(N, m.K, 1, false);
+    use_split(p, ws, at);
+    const dim3 grid(static_cast<unsigned>((p.kb + 7) / 8), static_cast<unsigned>(N));
+    mx_split_kernel<<<grid, 256, 0, s>>>(m.X, p.kb, reinterpret_cast<__half*>(ws + at.b),
+                                         reinterpret_cast<float*>(ws + at.s));
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_few<GQ_TYPE_MXFP4, kDense, 1>(p, (N + kFewGroup - 1) / kFewGroup, info, s);
+    if (N <= 8) return launch_few<GQ_TYPE_MXFP4, kDense, 1, 1>(p, 1, info, s);
+    return launch_few<GQ_TYPE_MXFP4, kDense, 1, 2>(p, (N + 15) / 16, info, s);
 }
 
 // ---- Mixture of experts -----------------------------------------------------------------
@@ -990,8 +1012,12 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const int64_t n = std::min(per, m.N - n0);
         const MoeSpace at = moe_space(m, n);
         const int pairs = static_cast<int>(n * m.top_k);
-        // groups there can be: every pair its own expert, or full groups over few experts
-        const int64_t groups = std::min<int64_t>(pairs, m.E + pairs / kFewGroup);
+        // One tile of 8 tokens, or two where an expert at work has more on average than fit one
+        // in most cases; `groups` as if the pairs were spread by chance.
+        const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
+        const double mean = pairs / active;
+        const bool wide = mean > 6.0;
+        const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(active * std::max(1.0, mean / 16) + 0.5));
         Params g{};
         g.W = m.W_gate;
         g.W2 = m.W_up;
@@ -999,15 +1025,15 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         g.total_bytes = g.row_bytes * m.F * m.E;
         g.rows = static_cast<int>(m.F);
         g.kb = static_cast<int>(m.D / 32);
-        g.xb = reinterpret_cast<const uint4*>(ws + at.xb);
-        g.xm = reinterpret_cast<const float*>(ws + at.xm);
-        g.N = n;
+        use_split(g, ws, at.x);
+        g.N = static_cast<int>(n);
         g.E = static_cast<int>(m.E);
         g.top_k = m.top_k;
         g.pairs = pairs;
         g.ids = m.ids + n0 * m.top_k;
-        g.hb = reinterpret_cast<__half*>(ws + at.hb);
-        g.hm = reinterpret_cast<float2*>(ws + at.hm);
+        g.hb = reinterpret_cast<__half*>(ws + at.h_at + at.h.b);
+        g.hs = reinterpret_cast<float*>(ws + at.h_at + at.h.s);
+        g.hsum = reinterpret_cast<float*>(ws + at.h_at + at.h.sum);
         g.h_type = m.t_down;
         Params d = g;
         d.W = m.W_down;
@@ -1016,18 +1042,15 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         d.total_bytes = d.row_bytes * m.D * m.E;
         d.rows = static_cast<int>(m.D);
         d.kb = static_cast<int>(m.F / 32);
-        d.xb = reinterpret_cast<const uint4*>(ws + at.hb);
-        d.xm = reinterpret_cast<const float*>(ws + at.hm);
-        d.part = reinterpret_cast<float*>(ws + at.part);
-        e = launch_split(m.X + n0 * m.D, n, g.kb, m.t, reinterpret_cast<__half*>(ws + at.xb),
-                         reinterpret_cast<float2*>(ws + at.xm), info, s);
-        if (e == cudaSuccess) e = launch_typed<kGateUp>(m.t, g, groups, info, s);
-        if (e == cudaSuccess) e = launch_typed<kDown>(m.t_down, d, groups, info, s);
+        use_split(d, ws + at.h_at, at.h);
+        d.out = reinterpret_cast<float*>(ws + at.part);
+        e = launch_split(m.X + n0 * m.D, n, g.kb, m.t, ws, at.x, s);
+        if (e == cudaSuccess) e = launch_typed<kGateUp>(m.t, g, wide, groups, info, s);
+        if (e == cudaSuccess) e = launch_typed<kDown>(m.t_down, d, wide, groups, info, s);
         if (e == cudaSuccess) {
-            const int64_t blocks = (n * (m.D / 4) + 255) / 256;
-            e = launch_after(combine_kernel, static_cast<unsigned>(std::min<int64_t>(blocks, info->sm_count * 8)),
-                             256, 0, s, static_cast<const float*>(d.part), g.ids, m.weights + n0 * m.top_k,
-                             n, m.top_k, g.E, d.rows, m.Y + n0 * m.D);
+            const dim3 grid(static_cast<unsigned>((m.D / 4 + 255) / 256), static_cast<unsigned>(n));
+            e = launch_after(combine_kernel, grid, 256, 0, s, static_cast<const float*>(d.out), g.ids,
+                             m.weights + n0 * m.top_k, m.top_k, g.E, d.rows, m.Y + n0 * m.D);
         }
         if (e != cudaSuccess) return e;
     }

@@ -1,11 +1,12 @@
 // gq_few.cuh -- what the few-token kernels (gq_few.cu) and their callers share: the split
 // activation format, its element order, and the launchers.
 //
-// Split activations. One 32-element block of one activation row becomes
-//   2 x 32 fp16   hi and lo with x = 2^(e - 14) (hi + lo), e = floor(log2 max |x|): the block
-//                 maximum lands in [2^14, 2^15), so hi keeps 11 significant bits and lo the
-//                 next 11 of every element down to 2^-38 of the block maximum;
-//   one float2    {scale 2^(e - 14), the block's sum (Q4_K's mins multiply it)}.
+// Split activations. One 32-element block of one activation row becomes 2 x 32 fp16, hi and lo,
+// with x = 2^(e - 14) (hi + lo): e = floor(log2 max |x|) over the row (of the hidden vector of an
+// expert: over the block, which is all that the kernel that makes it sees). The maximum lands in
+// [2^14, 2^15), so hi keeps 11 significant bits of every element and lo the next 11, down to
+// 2^-39 of the maximum. With them the scale 2^(e - 14) and, where Q4_K's mins multiply them, the
+// sums of the blocks (of a row with one scale: before it).
 // The weights enter the tensor cores as exact fp16 integers (or E2M1 values), so a product's
 // only rounding beside the fp32 sums is the 2^-22 of hi + lo.
 //
@@ -21,7 +22,6 @@
 
 namespace gq {
 
-constexpr int kFewGroup = 8;   // tokens per pass over the weights
 
 // Place (0..31) of element i of a block in the order in which the four lanes that share a
 // weight row hold it: lane t = place / 8 takes the block's bytes 4t..4t+3 (and 16 + 4t.. for

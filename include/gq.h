@@ -169,8 +169,9 @@ gq_status gq_quantize_q4_k(const float* W, int64_t M, int64_t K, void* W_blocks,
  * with an infinity or a NaN gets s = 255 and codes 0: all its weights read back as NaN.
  * Bit-for-bit reproducible. K must be a multiple of 32; K and M are otherwise free.
  * The mul_mat entry points take MXFP4 for every N, to fp32 accuracy (X is split in two fp16
- * terms, 22 bits): |Y - Y_exact| <= (K / 32 + 160) 2^-24 sum_k |What[m][k] X[n][k]|, the
- * roundings of X's terms and of the fp32 sums. Each needs a
+ * terms, 22 bits, under one scale a row): |Y - Y_exact| <= (K / 32 + 160) 2^-24
+ * sum_k |What[m][k] X[n][k]| + 2^-38 max|X[n]| sum_k |What[m][k]|, the roundings of the fp32
+ * sums and of X's terms. Each needs a
  * workspace (gq_mul_mat_workspace_size); the forms that use the library's refuse to be captured
  * into a graph (GQ_ERR_CUDA), the _ws forms and gq_mul_mat_noalloc do not. gq_mul_mat_batched
  * runs MXFP4 problems one after another. gq_mul_mat_rmsnorm and gq_mul_mat_swiglu take it in
@@ -220,8 +221,7 @@ gq_status gq_mul_mat(const void* W_blocks, gq_type t, int64_t M, int64_t K,
  * for the X block sums), plus 2 * 256 * 128 * P * 4 + 4096 for the partial sums (and
  * their counters) of tiles whose k range is split between CTAs;
  * N * K * 2 (a bf16 copy of X, rounded up to 256) on the prefill path (N >= 65). MXFP4, for
- * every N: N' * K * 4 + N' * K / 4 for the split X of N' = min(N, 4096) tokens (each part
- * rounded up to 256).
+ * every N: N' (4 K + K / 8) bytes and 9 KB for the split X of N' = min(N, 4096) tokens.
  * Tensor-core paths need K a multiple of 256. 0 for invalid arguments.
  */
 size_t gq_mul_mat_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N);
@@ -255,7 +255,7 @@ gq_status gq_mul_mat_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K,
  *     exceeds 64 MiB (N * K > 32 Mi) return GQ_ERR_SHAPE;
  *   - the tensor-core decode (3 <= N <= 64) needs at most 64 * K * 2 bytes + 16 MiB + 4 KiB
  *     there; a larger K (beyond ~390k) runs on the CUDA-core decode kernels instead;
- *   - MXFP4 takes its tokens in as many passes as the array makes necessary (4.25 K bytes a
+ *   - MXFP4 takes its tokens in as many passes as the array makes necessary (4.125 K bytes a
  *     token; GQ_ERR_SHAPE when one token does not fit);
  *   - the first call on a device looks up that array's device address (a one-time host-side
  *     set-up). The address is kept for the life of the process, so libgq must not be used
@@ -425,7 +425,8 @@ typedef struct gq_moe_experts {
  *     the chosen experts' weights (three launches), more in several.
  *   - Accuracy: fp32. X and the hidden vector are split in two fp16 terms (22 bits) and every
  *     sum is held in fp32: each product's error is at most (K / 32 + 160) 2^-24
- *     sum_k (|What| + |z|) |x|, z = dmin m for Q4_K (0 for the other types), carried on as in gq_mul_mat_swiglu. Results are deterministic.
+ *     sum_k (|What| + |z|) |x| + 2^-38 max|x| sum_k (|What| + |z|), z = dmin m for Q4_K (0 for
+ *     the other types), carried on as in gq_mul_mat_swiglu. Results are deterministic.
  *   - Only the weights of chosen experts are read, once per group of up to 16 tokens.
  * Workspaces as for gq_mul_mat_mx4x: gq_moe_swiglu uses the library's (not in a capture),
  * gq_moe_swiglu_ws the caller's gq_moe_workspace_size bytes.

@@ -16,8 +16,11 @@ def test_sizes(gq_lib):
     assert gq_lib.TYPES["mxfp4"] == 39 and lib.gq_block_bytes(39) == 17
     assert lib.gq_row_bytes(39, 2048) == 64 * 17 and lib.gq_row_bytes(39, 40) == 0
     assert lib.gq_mul_mat_workspace_size(39, 64, 256, 0) == 0
-    assert lib.gq_mul_mat_workspace_size(39, 64, 256, 3) == 3 * 256 * 4 + 256
-    assert lib.gq_mul_mat_workspace_size(39, 64, 256, 5000) == 4096 * 256 * 4 + 4096 * 64
+    size = lib.gq_mul_mat_workspace_size
+    for K, N in ((256, 3), (2048, 1), (32, 4096), (5632, 100)):
+        n = N * (4 * K + K // 8)
+        assert n < size(39, 64, K, N) <= n + 9 * 1024 and size(39, 64, K, N) % 256 == 0
+    assert size(39, 64, 256, 5000) == size(39, 64, 256, 4096)
     assert lib.gq_mul_mat_mx4x_workspace_size(2, 64, 256, 3) == 0
     assert lib.gq_mul_mat_mx4x_workspace_size(39, 64, 256, 3) > 0
 
