@@ -29,6 +29,8 @@ Q4_K = 12
 MXFP4 = 39
 TYPES = {"q4_0": Q4_0, "q8_0": Q8_0, "q4_k": Q4_K, "mxfp4": MXFP4, Q4_0: Q4_0, Q8_0: Q8_0,
          Q4_K: Q4_K, MXFP4: MXFP4}
+_QUANTIZE = {Q4_0: "gq_quantize_q4_0", Q8_0: "gq_quantize_q8_0", Q4_K: "gq_quantize_q4_k",
+             MXFP4: "gq_quantize_mxfp4"}
 MAX_BATCH = 256
 
 STATUS = {0: "GQ_OK", -1: "GQ_ERR_NULL", -2: "GQ_ERR_SHAPE", -3: "GQ_ERR_TYPE",
@@ -178,9 +180,17 @@ def _type(t) -> int:
         raise ValueError(f"unknown block type {t!r}") from None
 
 
+# torch's current stream of a device as an address, without building a Stream object for it
+# (2.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
@@ -226,8 +236,7 @@ def quantize(W: torch.Tensor, t, out: torch.Tensor | None = None, stream=None) -
     M, K = W.shape
     if out is None:
         out = torch.empty((M, row_bytes(t, K)), dtype=torch.uint8, device=W.device)
-    fn = {Q4_0: lib.gq_quantize_q4_0, Q8_0: lib.gq_quantize_q8_0,
-          Q4_K: lib.gq_quantize_q4_k, MXFP4: lib.gq_quantize_mxfp4}[_type(t)]
+    fn = getattr(lib, _QUANTIZE[_type(t)])
     _check(fn(_dev(W, torch.float32, "W"), M, K, _dev(out, torch.uint8, "W_blocks"),
               _stream(stream)), "gq_quantize")
     return out
@@ -401,20 +410,32 @@ def mul_mat_q8x_batched(problems, t, N: int, stream=None) -> None:
 
 def _call_stream(stream, *tensors) -> int:
     """The stream of a call on these tensors: CUDA ones must live on the current device, where
-    the library launches."""
+    the library launches (get_device() is -1 for host memory)."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t.is_cuda and t.get_device() != dev:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+        at = t.get_device()
+        if at != dev and at >= 0:
+            raise ValueError(f"tensor on cuda:{at}, but the current device is cuda:{dev}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
     return _stream(stream)
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
     """An output of a call on `stream` (None: torch's current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     out = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:   # else its memory could be handed on before the call has written it
-        out.record_stream(stream)
+    out.record_stream(stream)   # else its memory could be handed on before the call has written it
     return out
+
+
+_BLOCKS = {Q4_0: (32, 18), Q8_0: (32, 34), Q4_K: (256, 144), MXFP4: (32, 17)}
+
+
+def _matrix_bytes(t: int, rows: int, K: int) -> int:
+    n, nb = _BLOCKS[t]
+    return rows * (K // n) * nb
 
 
 def _tokens(X: torch.Tensor, K: int, name: str = "X") -> torch.Tensor:
@@ -437,11 +458,12 @@ def mul_mat_mx4x(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     `workspace` (uint8 CUDA tensor of mx4x_workspace_size bytes) the call can be captured."""
     X = _tokens(X, K)
     N = X.shape[0]
-    _has(blocks, M * row_bytes(t, K), "W_blocks")
+    t = _type(t)
+    _has(blocks, _matrix_bytes(t, M, K), "W_blocks")
     if out is None:
         out = _new((N, M), torch.float32, X.device, stream) if X.is_cuda else _out_like(X, (N, M))
     _has(out, N * M, "Y")
-    args = (_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K, _act(X, torch.float32, "X"), N,
+    args = (_dev(blocks, torch.uint8, "W_blocks"), t, M, K, _act(X, torch.float32, "X"), N,
             _act(out, torch.float32, "Y"))
     s = _call_stream(stream, blocks, X, out)
     if workspace is None:
@@ -463,10 +485,13 @@ def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, stream=None
         raise ValueError("logits must be (N, E)")
     N, E = logits.shape
     p = _dev(logits, torch.float32, "logits")
-    ids = _new((N, max(0, top_k)), torch.int32, logits.device, stream)
-    weights = _new((N, max(0, top_k)), torch.float32, logits.device, stream)
-    _check(lib.gq_moe_route(p, N, E, top_k, int(renorm), ids.data_ptr(), weights.data_ptr(),
-                            _call_stream(stream, logits)), "gq_moe_route")
+    shape, device = (N, max(0, top_k)), logits.device
+    ids = _new(shape, torch.int32, device, stream)
+    weights = _new(shape, torch.float32, device, stream)
+    status = lib.gq_moe_route(p, N, E, top_k, 1 if renorm else 0, ids.data_ptr(), weights.data_ptr(),
+                              _call_stream(stream, logits))
+    if status:
+        _check(status, "gq_moe_route")
     return ids, weights
 
 
@@ -476,15 +501,16 @@ class MoeExperts:
 
     def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, t, E: int, D: int,
                  F: int, t_down=None):
-        t_down = t if t_down is None else t_down
-        for w, n, name in ((gate, E * F * row_bytes(t, D), "W_gate"),
-                           (up, E * F * row_bytes(t, D), "W_up"),
-                           (down, E * D * row_bytes(t_down, F), "W_down")):
-            _has(w, n, name)
+        t = _type(t)
+        t_down = t if t_down is None else _type(t_down)
+        n = _matrix_bytes(t, E * F, D)
+        _has(gate, n, "W_gate")
+        _has(up, n, "W_up")
+        _has(down, _matrix_bytes(t_down, E * D, F), "W_down")
         self.E, self.D, self.F = E, D, F
         self.tensors = (gate, up, down)   # kept alive: the struct holds raw pointers
         self.c = Experts(_dev(gate, torch.uint8, "W_gate"), _dev(up, torch.uint8, "W_up"),
-                         _dev(down, torch.uint8, "W_down"), _type(t), _type(t_down), E, D, F)
+                         _dev(down, torch.uint8, "W_down"), t, t_down, E, D, F)
 
     def workspace_size(self, N: int, top_k: int) -> int:
         return int(lib.gq_moe_workspace_size(ctypes.byref(self.c), N, top_k))

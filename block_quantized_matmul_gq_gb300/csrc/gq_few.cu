@@ -25,7 +25,9 @@
 // its own ring of 16-byte asynchronous copies, four lanes to a weight row: a row's chunk from
 // the word that holds its first byte, because rows of 17- and 18-byte blocks start anywhere; the
 // words are aligned in registers. The ring runs on across units, and weights do not depend on
-// the kernel before, so they start to stream before griddepcontrol.wait.
+// the kernel before, so they start to stream before griddepcontrol.wait. (They, and ids, come
+// from before the call: the split kernel, which every call begins with, waits for all that came
+// before it on the stream, and only then lets this kernel start.)
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -214,14 +216,21 @@ template <int T, int Terms, int NT, bool Scaled>
 __device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const float (&d)[2],
                                                const float (&m)[2], const Columns<NT, Terms>& col,
                                                float (&tot)[NT][4]) {
-    float c[NT][4];
+    // one column tile: hi and lo in chains of their own, to be added at the end
+    constexpr bool kTwo = Terms == 2 && NT == 1;
+    float c[NT][4], l[4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][0].x, col.b[n][0].y);
+    if constexpr (kTwo) mma_first(l, q[0][0], q[1][0], q[0][1], q[1][1], col.b[0][1].x, col.b[0][1].y);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][0].z, col.b[n][0].w);
-    if constexpr (Terms == 2) {
+    if constexpr (kTwo) {
+        mma_next(l, q[0][2], q[1][2], q[0][3], q[1][3], col.b[0][1].z, col.b[0][1].w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[0][i] += l[i];
+    } else if constexpr (Terms == 2) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             mma_next(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][1].x, col.b[n][1].y);
@@ -338,6 +347,9 @@ struct Worker {
     static constexpr bool kSums = T == GQ_TYPE_Q4_K;
     static constexpr int kSub = M == kGateUp ? 2 : 1;   // a unit's passes: 16 gate and 16 up rows each
     static constexpr int kTotals = 2 * NT * 4;   // a lane's, of one pass
+    // Blocks whose activations are in registers ahead of their use: an L2 access takes 600 cycles,
+    // a warp's block about 130.
+    static constexpr int kDepth = NT == 1 ? 4 : 2;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kSumBytes = kWarps * kTotals * 32 * 4;
     static constexpr int kListBytes = M == kDense ? 0 : static_cast<int>(sizeof(Lists));
@@ -352,7 +364,7 @@ struct Worker {
     int lane, wk, wr, kwarps;
     // the next chunk to copy: unit (group, tile, how many are left), pass, chunk; stage
     int fgi, ftile, fleft, fs, fc, fstage;
-    int64_t frow;       // its first weight row
+    int64_t fbyte;      // where its first weight row begins
 
     __device__ __forceinline__ int expert_of(int gi) const { return M == kDense ? 0 : L.expert[gi]; }
     __device__ __forceinline__ int count_of(int gi) const {
@@ -365,7 +377,7 @@ struct Worker {
     }
 
     __device__ __forceinline__ void copy_row() {
-        frow = static_cast<int64_t>(expert_of(fgi)) * p.rows + ftile * 32 + fs * 16;
+        fbyte = (static_cast<int64_t>(expert_of(fgi)) * p.rows + ftile * 32 + fs * 16) * p.row_bytes;
     }
 
     // Starts the copies of the next chunk (if any), as one group. Staged row 8 j + g
@@ -375,7 +387,7 @@ struct Worker {
     __device__ __forceinline__ void issue() {
         if (fleft > 0) {
             const int l = lane & 3;
-            const int64_t chunk = frow * p.row_bytes + fc * (kCB * kBB);
+            const int64_t chunk = fbyte + fc * (kCB * kBB);
             const uint32_t dst = ring + fstage * kStageBytes + (lane >> 2) * kPitch + 16 * l;
             if (ftile * 32 + 32 <= p.rows && chunk + 31 * p.row_bytes + 16 * kWords <= p.total_bytes) {
                 int64_t at = chunk + (lane >> 2) * p.row_bytes;
@@ -453,69 +465,86 @@ struct Worker {
         }
     }
 
-    // One block of the 32 staged rows, whose first byte lies `pos` bytes into every row.
-    __device__ __forceinline__ void block(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int pos,
-                                          const Cols& col) const {
-        // Rows agree in the low two bits of their places (eight rows are a multiple of 8 bytes):
-        // the aligned word before a code word, and the shift that takes the word out of two.
+    // The codes and scales of one block of the 32 staged rows, as they are.
+    struct Raw {
+        uint32_t w[2][2][T == GQ_TYPE_Q8_0 ? 2 : 1], d[2][2];
+    };
+
+    // The block whose first byte lies `pos` bytes into every row. Rows agree in the low two bits
+    // of their places (eight rows are a multiple of 8 bytes): the aligned word before a code
+    // word, and the shift that takes the word out of two.
+    __device__ __forceinline__ void fetch(Raw& x, const uint32_t (&base)[2][2], int pos) const {
         constexpr int kHead = T == GQ_TYPE_MXFP4 ? 1 : 2;
         const uint32_t r = (base[0][0] + pos + kHead) & 3u;
         const int off = pos + kHead - static_cast<int>(r) + 4 * (lane & 3);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = base[mt][h] + off;
+                x.w[mt][h][0] = __funnelshift_r(lds32(at), lds32(at + 4), r << 3);
+                if constexpr (T == GQ_TYPE_Q8_0)
+                    x.w[mt][h][1] = __funnelshift_r(lds32(at + 16), lds32(at + 20), r << 3);
+                x.d[mt][h] = T == GQ_TYPE_MXFP4 ? lds8(base[mt][h] + pos) : lds16(base[mt][h] + pos);
+            }
+    }
+
+    __device__ __forceinline__ void multiply(float (&tot)[2][NT][4], const Raw& x, const Cols& col) const {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             uint32_t q[2][4];
             float d[2], m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t at = base[mt][h] + off;
-                const uint32_t w0 = __funnelshift_r(lds32(at), lds32(at + 4), r << 3);
                 if constexpr (T == GQ_TYPE_Q8_0) {
-                    const uint32_t w1 = __funnelshift_r(lds32(at + 16), lds32(at + 20), r << 3);
-                    const uint32_t u0 = w0 ^ 0x80808080u, u1 = w1 ^ 0x80808080u;
+                    const uint32_t u0 = x.w[mt][h][0] ^ 0x80808080u, u1 = x.w[mt][h][1] ^ 0x80808080u;
                     // 1024 + 128 + code, byte by byte under the exponent
                     q[h][0] = h2_sub(__byte_perm(u0, 0x64u, 0x4140), 0x64806480u);
                     q[h][1] = h2_sub(__byte_perm(u0, 0x64u, 0x4342), 0x64806480u);
                     q[h][2] = h2_sub(__byte_perm(u1, 0x64u, 0x4140), 0x64806480u);
                     q[h][3] = h2_sub(__byte_perm(u1, 0x64u, 0x4342), 0x64806480u);
                 } else if constexpr (T == GQ_TYPE_Q4_0) {
-                    nibbles_to_f16<8>(w0, q[h]);
+                    nibbles_to_f16<8>(x.w[mt][h][0], q[h]);
                 } else {
-                    e2m1_to_f16(w0, q[h]);
+                    e2m1_to_f16(x.w[mt][h][0], q[h]);
                 }
-                if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(lds16(base[mt][h] + pos));
+                if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(x.d[mt][h]);
             }
-            if constexpr (T == GQ_TYPE_MXFP4)
-                e8m0_to_f32(lds8(base[mt][0] + pos), lds8(base[mt][1] + pos), d[0], d[1]);
+            if constexpr (T == GQ_TYPE_MXFP4) e8m0_to_f32(x.d[mt][0], x.d[mt][1], d[0], d[1]);
             block_products<T, Terms, NT, kScaled>(q, d, m, col, tot[mt]);
         }
     }
 
-    // Q4_K: sub-blocks 2 j and 2 j + 1, which share code bytes, s = 0 or 1 of them.
-    __device__ __forceinline__ void block_q4k(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int j, int s,
-                                              const Cols& col) const {
+    // Q4_K: sub-blocks 2 j and 2 j + 1, which share code bytes (low and high nibbles).
+    __device__ __forceinline__ void pair_q4k(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int j,
+                                             const Cols& c0, const Cols& c1) const {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            uint32_t q[2][4];
-            float d[2], m[2];
+            uint32_t q[2][2][4];
+            float d[2][2], m[2][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint4 hd = lds128(base[mt][h]);
                 const uint32_t at = base[mt][h] + 16 + 32 * j + 4 * (lane & 3);
-                const uint32_t w0 = lds32(at), w1 = lds32(at + 16);
-                const uint32_t mask = s ? 0x00F000F0u : 0x000F000Fu;
-                q[h][0] = (w0 & mask) | kMagic;
-                q[h][1] = ((w0 >> 8) & mask) | kMagic;
-                q[h][2] = (w1 & mask) | kMagic;
-                q[h][3] = ((w1 >> 8) & mask) | kMagic;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    q[h][i] = s ? h2_fma(q[h][i], kSixteenth, 0xD400D400u) : h2_sub(q[h][i], kMagic);
+                const uint32_t w0 = lds32(at), w1 = lds32(at + 16), v0 = w0 >> 8, v1 = w1 >> 8;
+                q[0][h][0] = h2_sub((w0 & 0x000F000Fu) | kMagic, kMagic);
+                q[0][h][1] = h2_sub((v0 & 0x000F000Fu) | kMagic, kMagic);
+                q[0][h][2] = h2_sub((w1 & 0x000F000Fu) | kMagic, kMagic);
+                q[0][h][3] = h2_sub((v1 & 0x000F000Fu) | kMagic, kMagic);
+                q[1][h][0] = h2_fma((w0 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
+                q[1][h][1] = h2_fma((v0 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
+                q[1][h][2] = h2_fma((w1 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
+                q[1][h][3] = h2_fma((v1 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
                 uint32_t sc, mn;
                 q4k_scales(hd, j, sc, mn);
-                d[h] = half_bits_to_float(hd.x) * byte_to_float(sc, s);
-                m[h] = half_bits_to_float(hd.x >> 16) * byte_to_float(mn, s);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    d[s][h] = half_bits_to_float(hd.x) * byte_to_float(sc, s);
+                    m[s][h] = half_bits_to_float(hd.x >> 16) * byte_to_float(mn, s);
+                }
             }
-            block_products<T, Terms, NT, kScaled>(q, d, m, col, tot[mt]);
+            block_products<T, Terms, NT, kScaled>(q[0], d[0], m[0], c0, tot[mt]);
+            block_products<T, Terms, NT, kScaled>(q[1], d[1], m[1], c1, tot[mt]);
         }
     }
 
@@ -523,7 +552,8 @@ struct Worker {
         const int n_tok = count_of(gi);
         const int g = lane >> 2, t = lane & 3;
         const uint32_t e_row = static_cast<uint32_t>(expert_of(gi)) * static_cast<uint32_t>(p.rows) + tile * 32;
-        float hidden[NT][2][4];   // kGateUp: tokens 2t, 2t + 1 x rows g, 8 + g of either pass
+        // kGateUp: the unit's hidden values, [token][row], in this warp's part of the sums
+        float* const hidden = sums + wr * kwarps * kTotals * 32;
 #pragma unroll 1
         for (int s = 0; s < kSub; ++s) {
             // Columns of tokens that the group does not have read token 0's: nothing uses them.
@@ -543,10 +573,10 @@ struct Worker {
             float tot[2][NT][4];
 #pragma unroll
             for (int i = 0; i < kTotals; ++i) (&tot[0][0][0])[i] = 0.0f;
-            Cols col[2];
+            Cols col[kDepth];
             const int jump = (kwarps - 1) * kCB + 1;   // from a chunk's last block to the next's first
-            load(col[0], acts, 1);
-            load(col[1], acts, kCB > 2 ? 1 : jump);
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i) load(col[i], acts, (i + 1) % kCB ? 1 : jump);
 #pragma unroll 1
             for (int c = wk; c < p.chunks; c += kwarps) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -562,23 +592,40 @@ struct Worker {
                         base[mt][h] = ring + stage * kStageBytes + (16 * mt + 8 * h + g) * kPitch +
                                       ((row * static_cast<uint32_t>(p.row_bytes) + static_cast<uint32_t>(c) * (kCB * kBB)) & 15u);
                     }
-                // pairs of blocks; a column set is loaded again as soon as it has been used
+                // A column set is loaded again as soon as it has been used; codes are fetched a
+                // block ahead (behind the chunk: bytes of the stage that are not used).
+                if constexpr (T == GQ_TYPE_Q4_K) {
 #pragma unroll 1
-                for (int b = 0; b + 1 < nb; b += 2) {
-                    const int step = b + 4 == nb ? jump : 1;   // block b + 3 ends the chunk
-                    if constexpr (T == GQ_TYPE_Q4_K)
-                        block_q4k(tot, base, b >> 1, 0, col[0]);
-                    else
-                        block(tot, base, b * kBB, col[0]);
-                    load(col[0], acts, 1);
-                    if constexpr (T == GQ_TYPE_Q4_K)
-                        block_q4k(tot, base, b >> 1, 1, col[1]);
-                    else
-                        block(tot, base, (b + 1) * kBB, col[1]);
-                    load(col[1], acts, step);
+                    for (int b = 0; b < kCB; b += kDepth) {
+                        const int step = (b + 2 * kDepth) % kCB ? 1 : jump;   // past a chunk's end
+#pragma unroll
+                        for (int i = 0; i < kDepth; i += 2) {
+                            pair_q4k(tot, base, (b + i) >> 1, col[i], col[i + 1]);
+                            load(col[i], acts, 1);
+                            load(col[i + 1], acts, i + 2 < kDepth ? 1 : step);
+                        }
+                    }
+                } else {
+                    Raw raw[2];
+                    fetch(raw[0], base, 0);
+#pragma unroll 1
+                    for (int b = 0; b + kDepth <= nb; b += kDepth) {
+                        const int step = (b + 2 * kDepth) % kCB ? 1 : jump;
+#pragma unroll
+                        for (int i = 0; i < kDepth; ++i) {
+                            fetch(raw[(i + 1) & 1], base, (b + i + 1 < kCB ? b + i + 1 : 0) * kBB);
+                            multiply(tot, raw[i & 1], col[i]);
+                            load(col[i], acts, i + 1 < kDepth ? 1 : step);
+                        }
+                    }
+                    const int rest = nb & (kDepth - 1);   // only in a row's last chunk
+#pragma unroll
+                    for (int i = 0; i + 1 < kDepth; ++i)
+                        if (i < rest) {
+                            fetch(raw[0], base, (nb - rest + i) * kBB);
+                            multiply(tot, raw[0], col[i]);
+                        }
                 }
-                if constexpr (T != GQ_TYPE_Q4_K)
-                    if (nb & 1) block(tot, base, (nb - 1) * kBB, col[0]);   // only a row's last chunk
                 __syncwarp();   // every lane has read its part of the stage
                 issue();
                 stage ^= 1;
@@ -591,9 +638,10 @@ struct Worker {
                     for (int i = 0; i < 4; ++i) {
                         const int tok = 8 * n + 2 * t + (i & 1);
                         const float sc = p.xs[x_row(gi, tok < n_tok ? tok : 0)];
-                        const float gate = tot[0][n][i] * sc, v = gate / (1.0f + expf(-gate)) * (tot[1][n][i] * sc);
-                        if (s == 0) hidden[n][i & 1][i >> 1] = v;
-                        else hidden[n][i & 1][2 + (i >> 1)] = v;
+                        const float gate = tot[0][n][i] * sc;
+                        if (wk == 0)
+                            hidden[tok * 32 + 16 * s + 8 * (i >> 1) + g] =
+                                gate / (1.0f + expf(-gate)) * (tot[1][n][i] * sc);
                     }
             } else if (wk == 0) {
 #pragma unroll
@@ -612,45 +660,37 @@ struct Worker {
                     }
             }
         }
-        if constexpr (M == kGateUp)
-            if (wk == 0) {
+        if constexpr (M == kGateUp) {
+            // the tokens in turn by the unit's warps; lane i: element i of the block
+            unit_sync();
+            const int place = few_place(p.h_type, lane), hb = p.rows / 32;
+#pragma unroll 1
+            for (int tok = wk; tok < n_tok; tok += kwarps) {
+                const float h = hidden[tok * 32 + lane];
+                const int e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu));
+                const Split x(h, e);
+                const int64_t at = static_cast<int64_t>(L.pair[L.start[gi] + tok]) * hb + tile;
+                __half* out = p.hb + at * 64 + place + (place & ~7);   // hi and lo by eights
+                out[0] = x.hi;
+                out[8] = x.lo;
+                if (p.h_type == GQ_TYPE_Q4_K) {
+                    float sum = x.sum();
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (8 * n < n_tok) write_hidden(gi, tile, 8 * n + 2 * t + i, n_tok, hidden[n][i]);
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    if (lane == 0) p.hsum[at] = pow2f(e - 14) * sum;
+                }
+                if (lane == 0) p.hs[at] = pow2f(e - 14);
             }
+            unit_sync();
+        }
     }
 
-    // The split activations of token `tok`'s 32 hidden values of a unit; this lane has elements
-    // g, 8 + g, 16 + g and 24 + g.
-    __device__ __forceinline__ void write_hidden(int gi, int tile, int tok, int n_tok, const float (&h)[4]) const {
-        const int g = lane >> 2;
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const int e = block_exponent(amax);
-        const int64_t at = static_cast<int64_t>(tok < n_tok ? L.pair[L.start[gi] + tok] : 0) * (p.rows / 32) + tile;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Split s(h[i], e);
-            sum += s.sum();
-            if (tok < n_tok) {
-                const int place = few_place(p.h_type, 8 * i + g);
-                __half* out = p.hb + at * 64 + place + (place & ~7);   // hi and lo by eights
-                out[0] = s.hi;
-                out[8] = s.lo;
-            }
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (g == 0 && tok < n_tok) {
-            p.hs[at] = pow2f(e - 14);
-            p.hsum[at] = pow2f(e - 14) * sum;
-        }
+    // The warps that share a unit.
+    __device__ __forceinline__ void unit_sync() const {
+        if (kwarps == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * kwarps) : "memory");
     }
 
     // Adds the K warps' totals, in their order, into the first one's.
@@ -660,14 +700,14 @@ struct Worker {
 #pragma unroll
             for (int i = 0; i < kTotals; ++i) at[(wk * kTotals + i) * 32] = tot[i];
         }
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * kwarps) : "memory");
+        unit_sync();
         if (wk == 0) {
 #pragma unroll 1
             for (int k = 1; k < kwarps; ++k)
 #pragma unroll
                 for (int i = 0; i < kTotals; ++i) tot[i] += at[(k * kTotals + i) * 32];
         }
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * kwarps) : "memory");
+        unit_sync();
     }
 };
 
@@ -717,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 __global__ void __launch_bounds__(256)
 combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
                const float* __restrict__ weights, int top_k, int E, int D, float* __restrict__ Y) {
+    griddep_launch_dependents();
     griddep_wait();   // `part`, and Y, which the kernels before may still read as X
     const int n = blockIdx.y, quads = D / 4;
     const int r = blockIdx.x * 256 + threadIdx.x;
@@ -749,7 +790,8 @@ __global__ void __launch_bounds__(512)
 split_kernel(const float* __restrict__ X, int kb, int type, __half* __restrict__ xb, float* __restrict__ xs,
              float* __restrict__ xsum) {
     __shared__ uint32_t most[16];
-    griddep_launch_dependents();
+    griddep_wait();                // X, and the workspace that kernels before may still read
+    griddep_launch_dependents();   // only now: the next kernel reads ids and weights before it waits
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     const float* x = X + row * kb * 32;
@@ -781,17 +823,17 @@ split_kernel(const float* __restrict__ X, int kb, int type, __half* __restrict__
 // scale.
 __global__ void __launch_bounds__(256)
 mx_split_kernel(const float* __restrict__ X, int kb, __half* __restrict__ xb, float* __restrict__ xm) {
+    griddep_wait();
     griddep_launch_dependents();
     const int blk = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (blk >= kb) return;
     const int64_t b = static_cast<int64_t>(blockIdx.y) * kb + blk;
     const float x = X[b * 32 + lane];
     const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu));
-    uint32_t m = 0;
-    if (byte != 255) m = e2m1_code(fabsf(x) * mx_inverse_scale(byte));
-    const float mag = m < 4 ? 0.5f * static_cast<float>(m)
-                            : static_cast<float>(m < 6 ? m - 2 : 2 * m - 8);
-    xb[b * 32 + few_place(GQ_TYPE_MXFP4, lane)] = __float2half_rn(copysignf(mag, x));
+    const uint32_t c = byte == 255 ? 0u : e2m1_pair(x * mx_inverse_scale(byte), 0.0f);
+    uint32_t h[4];
+    e2m1_to_f16(c, h);
+    xb[b * 32 + few_place(GQ_TYPE_MXFP4, lane)] = __ushort_as_half(static_cast<unsigned short>(h[0]));
     if (lane == 0) xm[b] = mx_scale(byte);
 }
 
@@ -817,10 +859,9 @@ SplitSpace split_space(int64_t n, int64_t K, int terms, bool sums) {
 
 cudaError_t launch_split(const float* X, int64_t rows, int kb, int type, uint8_t* ws, const SplitSpace& at,
                          cudaStream_t s) {
-    split_kernel<<<static_cast<unsigned>(rows), 512, 0, s>>>(
-        X, kb, type, reinterpret_cast<__half*>(ws + at.b), reinterpret_cast<float*>(ws + at.s),
-        reinterpret_cast<float*>(ws + at.sum));
-    return cudaGetLastError();
+    return launch_after(split_kernel, dim3(static_cast<unsigned>(rows)), 512, 0, s, X, kb, type,
+                        reinterpret_cast<__half*>(ws + at.b), reinterpret_cast<float*>(ws + at.s),
+                        reinterpret_cast<float*>(ws + at.sum));
 }
 
 void use_split(Params& p, const uint8_t* ws, const SplitSpace& at) {
@@ -830,37 +871,22 @@ void use_split(Params& p, const uint8_t* ws, const SplitSpace& at) {
 }
 
 // log2 of the warps that split a unit's K. Every row warp takes the same number of units but for
-// one; the split that leaves the least idle wins, a join counting as 3 %.
-int pick_kshift(int64_t units, int chunks, int warps) {
+// one, so the split that leaves the fewest warps idle wins, less what a join costs: at 8 tokens a
+// unit 3 % a doubling (16 tokens over 64 Q8_0 experts: 1210 units, 103, 105 and 113 us with 2, 4
+// and 8 warps that all have work), at 16 tokens 8 % (61 over 64 Q4_K experts: 177, 181, 186 and
+// 198 us with 1, 2, 4 and 8 warps).
+int pick_kshift(int64_t units, int chunks, int warps, double join) {
     int best = 0;
     double most = -1.0;
     for (int ks = 0; ks <= 3 && (1 << ks) <= chunks; ++ks) {
-        const double rw = warps >> ks, rounds = static_cast<double>((units + (warps >> ks) - 1) / (warps >> ks));
-        const double use = units / (rw * rounds) - 0.03 * ks;
+        const int64_t rw = warps >> ks, rounds = (units + rw - 1) / rw;
+        const double use = static_cast<double>(units) / (rw * rounds) * (1.0 - join * ks);
         if (use > most) {
             most = use;
             best = ks;
         }
     }
     return best;
-}
-
-// A launch that may start while the kernel before it on the stream still runs (it waits with
-// griddep_wait).
-template <typename... Sig, typename... Args>
-cudaError_t launch_after(void (*kernel)(Sig...), dim3 grid, int threads, int smem, cudaStream_t s,
-                         const Args&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // `groups`: how many there are likely to be.
@@ -870,7 +896,7 @@ cudaError_t launch_few(Params p, int64_t groups, const DeviceInfo* info, cudaStr
     p.chunks = (p.kb + Fmt<T>::cb - 1) / Fmt<T>::cb;
     p.tiles = (p.rows + 31) / 32;
     const int64_t units = p.tiles * groups;
-    p.kshift = pick_kshift(units, p.chunks, 2 * info->sm_count * kWarps);
+    p.kshift = pick_kshift(units, p.chunks, 2 * info->sm_count * kWarps, NT == 1 ? 0.03 : 0.08);
     const int64_t rwarps = kWarps >> p.kshift;
     const unsigned grid = static_cast<unsigned>(
         std::max<int64_t>(1, std::min<int64_t>((units + rwarps - 1) / rwarps, int64_t(info->sm_count) * 2)));
@@ -988,9 +1014,8 @@ cudaError_t launch_few_mx4x(const MatProblem& m, int64_t N, void* workspace, cud
     const SplitSpace at = split_space(N, m.K, 1, false);
     use_split(p, ws, at);
     const dim3 grid(static_cast<unsigned>((p.kb + 7) / 8), static_cast<unsigned>(N));
-    mx_split_kernel<<<grid, 256, 0, s>>>(m.X, p.kb, reinterpret_cast<__half*>(ws + at.b),
-                                         reinterpret_cast<float*>(ws + at.s));
-    e = cudaGetLastError();
+    e = launch_after(mx_split_kernel, grid, 256, 0, s, m.X, p.kb, reinterpret_cast<__half*>(ws + at.b),
+                     reinterpret_cast<float*>(ws + at.s));
     if (e != cudaSuccess) return e;
     if (N <= 8) return launch_few<GQ_TYPE_MXFP4, kDense, 1, 1>(p, 1, info, s);
     return launch_few<GQ_TYPE_MXFP4, kDense, 1, 2>(p, (N + 15) / 16, info, s);

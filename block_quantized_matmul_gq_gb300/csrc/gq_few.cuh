@@ -53,11 +53,21 @@ __device__ __forceinline__ float pow2f(int e) {   // e in [-126, 127]
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// E2M1 code (0..7) of a magnitude already divided by its block scale: nearest value, ties to
-// the even code, above 6 saturates.
-__device__ __forceinline__ uint32_t e2m1_code(float a) {
-    return (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) +
-           (a > 5.0f);
+// Two values already divided by their block scale as one byte of E2M1 codes, `lo` in the low
+// nibble: nearest value, ties to the even code, beyond 6 saturates, the sign kept.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+        : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The code bytes 4q..4q+3 of a block from its elements 4q..4q+3 and 16+4q..16+4q+3.
+__device__ __forceinline__ uint32_t mx_codes(const float (&v)[8], float inv) {
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes |= e2m1_pair(v[i] * inv, v[4 + i] * inv) << (8 * i);
+    return codes;
 }
 
 // E8M0 scale byte of a block maximum (bits of a non-negative float): floor(log2 amax) - 2 with
@@ -75,6 +85,24 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
 // 2^(127 - byte) for byte <= 254.
 __device__ __forceinline__ float mx_inverse_scale(uint32_t byte) {
     return byte == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((254u - byte) << 23);
+}
+
+// A launch that may start while the kernel before it on the stream still runs (it waits with
+// griddep_wait).
+template <typename... Sig, typename... Args>
+cudaError_t launch_after(void (*kernel)(Sig...), dim3 grid, int threads, int smem, cudaStream_t s,
+                         const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace gq

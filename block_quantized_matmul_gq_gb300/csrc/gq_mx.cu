@@ -77,6 +77,7 @@ struct PrepareParams {
 // Weights: one thread per 17-byte block. X: four lanes per block (lane q: elements 4q..4q+3 and
 // 16+4q..), as in the quantizer. Rows and k that pad a record are zeros with scale 2^0.
 __global__ void __launch_bounds__(256) mx_prepare_kernel(const __grid_constant__ PrepareParams p) {
+    griddep_wait();   // X, and the records that a product before may still read
     griddep_launch_dependents();
     const int kpad = p.ktiles * kStageBlocks;
     if (blockIdx.x < p.w_ctas) {
@@ -150,15 +151,7 @@ __global__ void __launch_bounds__(256) mx_prepare_kernel(const __grid_constant__
         amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         if (i >= p.x_blocks) continue;
         const uint32_t byte = real ? mx_scale_byte(amax) : 127u;
-        uint32_t codes = 0;
-        if (real && byte != 255) {
-            const float inv = mx_inverse_scale(byte);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t c = e2m1_code(fabsf(v[k]) * inv) | ((__float_as_uint(v[k]) >> 31) << 3);
-                codes |= c << (k < 4 ? 8 * k : 8 * (k - 4) + 4);
-            }
-        }
+        const uint32_t codes = real && byte != 255 ? mx_codes(v, mx_inverse_scale(byte)) : 0u;
         const int tile = static_cast<int>(row / p.bn), r = static_cast<int>(row - int64_t(tile) * p.bn), j = kb & 7;
         uint8_t* rec = p.xrec + (static_cast<int64_t>(tile) * p.ktiles + (kb >> 3)) * record_bytes(p.bn);
         *reinterpret_cast<uint32_t*>(rec + code_at(r, j) + 4 * q) = codes;
@@ -381,18 +374,9 @@ cudaError_t launch_mx_gemm(const GemmParams& g, const DeviceInfo* info, cudaStre
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg{};
     const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, info->sm_count)));
-    cfg.blockDim = dim3(kMxThreads);
-    cfg.dynamicSmemBytes = Mx<BN>::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, g);
+    return launch_after(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, info->sm_count))), kMxThreads,
+                        Mx<BN>::kSmem, s, g);
 }
 
 }  // namespace
@@ -426,8 +410,7 @@ cudaError_t launch_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStr
     const int64_t most = int64_t(info->sm_count) * 8;
     p.w_ctas = std::min<int64_t>((p.w_blocks + 255) / 256, most);
     const int64_t x_ctas = std::min<int64_t>((p.x_blocks + 63) / 64, most);
-    mx_prepare_kernel<<<static_cast<unsigned>(p.w_ctas + x_ctas), 256, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(mx_prepare_kernel, dim3(static_cast<unsigned>(p.w_ctas + x_ctas)), 256, 0, s, p);
     if (e != cudaSuccess) return e;
     const GemmParams g{p.wrec, p.xrec, m.Y, m.M, N, p.ktiles, static_cast<int>(at.m_tiles),
                        static_cast<int>(at.n_tiles), info->status};

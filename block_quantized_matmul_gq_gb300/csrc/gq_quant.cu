@@ -220,63 +220,65 @@ dequantize_q4_k_kernel(const uint8_t* __restrict__ blocks, int64_t n_elems,
 // Both directions stream: 4 or 17/32 bytes a weight in, the other out, a few instructions a
 // weight, so DRAM bounds them. Four lanes share a block (lane q: elements 4q..4q+3 and
 // 16+4q..16+4q+3, i.e. code bytes 4q..4q+3), which makes the fp32 side two 16-byte accesses
-// a lane; a CTA's 64 blocks are 1088 bytes, a multiple of 16, so the 17-byte blocks pass
-// through shared memory and reach DRAM as whole 16-byte words whatever their offsets.
-constexpr int kMxTile = 64;                          // blocks per CTA step
-constexpr int kMxTileBytes = kMxTile * kMxfp4Bytes;  // 1088
+// a lane; a CTA's step of 256 blocks is 4352 bytes, a multiple of 16, so the 17-byte blocks pass
+// through shared memory and reach DRAM as whole 16-byte words whatever their offsets. A thread
+// has four blocks' quarters in flight at once (one at a time: 118 us for 32000 x 2048 to blocks
+// and back, 5.0 TB/s), or one where that would leave SMs without a CTA (256 x 2048: 3.9 against
+// 5.4 us). The codes come from the conversion instruction, two a byte as they are stored:
+// compared with the seven midpoints instead, the quantizer was bound by instructions (71 us
+// for 32000 x 2048).
+constexpr int kMxBlocks = kQuantThreads / 4;   // blocks that the threads of a CTA hold at once
 
 // Vec: W is 16-byte aligned (any 4-byte alignment is allowed).
-template <bool Vec>
+template <bool Vec, int kMxEach>
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_mxfp4_kernel(const float* __restrict__ W, int64_t n_blocks, uint8_t* __restrict__ out) {
+    constexpr int kMxTile = kMxEach * kMxBlocks, kMxTileBytes = kMxTile * kMxfp4Bytes;
     __shared__ __align__(16) uint8_t buf[2][kMxTileBytes];
     const int q = threadIdx.x & 3, b = threadIdx.x >> 2;
     int side = 0;
     for (int64_t tile = blockIdx.x; tile * kMxTile < n_blocks; tile += gridDim.x, side ^= 1) {
-        const int64_t block = tile * kMxTile + b;
-        float v[8] = {};
-        if (block < n_blocks) {
+        float v[kMxEach][8];
+#pragma unroll
+        for (int k = 0; k < kMxEach; ++k) {
+            const int64_t block = tile * kMxTile + k * kMxBlocks + b;
             const float* src = W + block * 32 + 4 * q;
-            if (Vec) {
+            if (block >= n_blocks) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+            } else if (Vec) {
                 const float4 lo = __ldcs(reinterpret_cast<const float4*>(src));
                 const float4 hi = __ldcs(reinterpret_cast<const float4*>(src + 16));
-                v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-                v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+                v[k][0] = lo.x; v[k][1] = lo.y; v[k][2] = lo.z; v[k][3] = lo.w;
+                v[k][4] = hi.x; v[k][5] = hi.y; v[k][6] = hi.z; v[k][7] = hi.w;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = src[i];
-                    v[4 + i] = src[16 + i];
+                    v[k][i] = src[i];
+                    v[k][4 + i] = src[16 + i];
                 }
             }
         }
-        uint32_t amax = 0;   // as bits: a NaN stays the largest
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        const uint32_t byte = mx_scale_byte(amax);
-        uint32_t codes = 0;
-        if (byte != 255) {
-            const float inv = mx_inverse_scale(byte);
+        for (int k = 0; k < kMxEach; ++k) {
+            uint32_t amax = 0;   // as bits: a NaN stays the largest
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t c =
-                    e2m1_code(fabsf(v[i]) * inv) | ((__float_as_uint(v[i]) >> 31) << 3);
-                codes |= c << (i < 4 ? 8 * i : 8 * (i - 4) + 4);
-            }
+            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const uint32_t byte = mx_scale_byte(amax);
+            const uint32_t codes = byte == 255 ? 0u : mx_codes(v[k], mx_inverse_scale(byte));
+            uint8_t* dst = buf[side] + (k * kMxBlocks + b) * kMxfp4Bytes;
+            if (q == 0) dst[0] = static_cast<uint8_t>(byte);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[1 + 4 * q + i] = static_cast<uint8_t>(codes >> (8 * i));
         }
-        uint8_t* dst = buf[side] + b * kMxfp4Bytes;
-        if (q == 0) dst[0] = static_cast<uint8_t>(byte);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[1 + 4 * q + i] = static_cast<uint8_t>(codes >> (8 * i));
         __syncthreads();   // two buffers: the next step writes the other one
         const int64_t left = n_blocks * kMxfp4Bytes - tile * kMxTileBytes;
         const int bytes = left < kMxTileBytes ? static_cast<int>(left) : kMxTileBytes;
         uint8_t* o = out + tile * kMxTileBytes;
-        if (threadIdx.x < bytes / 16)
-            reinterpret_cast<uint4*>(o)[threadIdx.x] =
-                reinterpret_cast<const uint4*>(buf[side])[threadIdx.x];
+        for (int i = threadIdx.x; i < bytes / 16; i += kQuantThreads)
+            __stcs(reinterpret_cast<uint4*>(o) + i, reinterpret_cast<const uint4*>(buf[side])[i]);
         if (threadIdx.x < (bytes & 15)) {
             const int at = (bytes & ~15) + threadIdx.x;
             o[at] = buf[side][at];
@@ -284,10 +286,11 @@ quantize_mxfp4_kernel(const float* __restrict__ W, int64_t n_blocks, uint8_t* __
     }
 }
 
-template <bool Vec>
+template <bool Vec, int kMxEach>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_mxfp4_kernel(const uint8_t* __restrict__ blocks, int64_t n_blocks,
                         float* __restrict__ out) {
+    constexpr int kMxTile = kMxEach * kMxBlocks, kMxTileBytes = kMxTile * kMxfp4Bytes;
     __shared__ __align__(16) uint8_t buf[2][kMxTileBytes];
     const int q = threadIdx.x & 3, b = threadIdx.x >> 2;
     int side = 0;
@@ -295,37 +298,40 @@ dequantize_mxfp4_kernel(const uint8_t* __restrict__ blocks, int64_t n_blocks,
         const int64_t left = n_blocks * kMxfp4Bytes - tile * kMxTileBytes;
         const int bytes = left < kMxTileBytes ? static_cast<int>(left) : kMxTileBytes;
         const uint8_t* src = blocks + tile * kMxTileBytes;
-        if (threadIdx.x < bytes / 16)
-            reinterpret_cast<uint4*>(buf[side])[threadIdx.x] =
-                __ldcs(reinterpret_cast<const uint4*>(src) + threadIdx.x);
+        for (int i = threadIdx.x; i < bytes / 16; i += kQuantThreads)
+            reinterpret_cast<uint4*>(buf[side])[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
         if (threadIdx.x < (bytes & 15)) {
             const int at = (bytes & ~15) + threadIdx.x;
             buf[side][at] = src[at];
         }
-        __syncthreads();
-        const int64_t block = tile * kMxTile + b;
-        if (block >= n_blocks) continue;
-        const uint8_t* blk = buf[side] + b * kMxfp4Bytes;
-        const float scale = mx_scale(blk[0]);
-        float v[8];
+        __syncthreads();   // two buffers: the next step writes the other one
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t c = i < 4 ? blk[1 + 4 * q + i] & 15u : blk[1 + 4 * q + i - 4] >> 4;
-            // E2M1 magnitudes 0, .5, 1, 1.5, then 2, 3, then 4, 6
-            const uint32_t m = c & 7u;
-            const float mag = m < 4 ? 0.5f * static_cast<float>(m)
-                                    : static_cast<float>(m < 6 ? m - 2 : 2 * m - 8);
-            v[i] = __uint_as_float(__float_as_uint(mag) | ((c & 8u) << 28)) * scale;
-        }
-        float* dst = out + block * 32 + 4 * q;
-        if (Vec) {
-            __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(reinterpret_cast<float4*>(dst + 16), make_float4(v[4], v[5], v[6], v[7]));
-        } else {
+        for (int k = 0; k < kMxEach; ++k) {
+            const int in = k * kMxBlocks + b;
+            const int64_t block = tile * kMxTile + in;
+            if (block >= n_blocks) continue;
+            const uint8_t* blk = buf[side] + in * kMxfp4Bytes;
+            const float scale = mx_scale(blk[0]);
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dst[i] = v[i];
-                dst[16 + i] = v[4 + i];
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c = i < 4 ? blk[1 + 4 * q + i] & 15u : blk[1 + 4 * q + i - 4] >> 4;
+                // E2M1 magnitudes 0, .5, 1, 1.5, then 2, 3, then 4, 6
+                const uint32_t m = c & 7u;
+                const float mag = m < 4 ? 0.5f * static_cast<float>(m)
+                                        : static_cast<float>(m < 6 ? m - 2 : 2 * m - 8);
+                v[i] = __uint_as_float(__float_as_uint(mag) | ((c & 8u) << 28)) * scale;
+            }
+            float* dst = out + block * 32 + 4 * q;
+            if (Vec) {
+                __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0], v[1], v[2], v[3]));
+                __stcs(reinterpret_cast<float4*>(dst + 16), make_float4(v[4], v[5], v[6], v[7]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dst[i] = v[i];
+                    dst[16 + i] = v[4 + i];
+                }
             }
         }
     }
@@ -346,11 +352,12 @@ cudaError_t launch_quantize(gq_type t, const float* W, int64_t n_blocks, uint8_t
     cudaError_t e = current_device_info(&info);
     if (e != cudaSuccess) return e;
     if (t == GQ_TYPE_MXFP4) {
-        const int g = grid_for(n_blocks, kMxTile, info);
-        if (reinterpret_cast<uintptr_t>(W) % 16 == 0)
-            quantize_mxfp4_kernel<true><<<g, kQuantThreads, 0, s>>>(W, n_blocks, out);
-        else
-            quantize_mxfp4_kernel<false><<<g, kQuantThreads, 0, s>>>(W, n_blocks, out);
+        const bool vec = reinterpret_cast<uintptr_t>(W) % 16 == 0;
+        const bool many = n_blocks >= int64_t(4) * kMxBlocks * info->sm_count;
+        const int g = grid_for(n_blocks, many ? 4 * kMxBlocks : kMxBlocks, info);
+        auto kernel = many ? (vec ? quantize_mxfp4_kernel<true, 4> : quantize_mxfp4_kernel<false, 4>)
+                           : (vec ? quantize_mxfp4_kernel<true, 1> : quantize_mxfp4_kernel<false, 1>);
+        kernel<<<g, kQuantThreads, 0, s>>>(W, n_blocks, out);
         return cudaGetLastError();
     }
     const int grid = grid_for(n_blocks, kQuantThreads / 32, info);
@@ -371,11 +378,12 @@ cudaError_t launch_dequantize(gq_type t, const uint8_t* blocks, int64_t n_elems,
     if (e != cudaSuccess) return e;
     if (t == GQ_TYPE_MXFP4) {
         const int64_t n_blocks = n_elems / 32;
-        const int g = grid_for(n_blocks, kMxTile, info);
-        if (reinterpret_cast<uintptr_t>(out) % 16 == 0)
-            dequantize_mxfp4_kernel<true><<<g, kQuantThreads, 0, s>>>(blocks, n_blocks, out);
-        else
-            dequantize_mxfp4_kernel<false><<<g, kQuantThreads, 0, s>>>(blocks, n_blocks, out);
+        const bool vec = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+        const bool many = n_blocks >= int64_t(4) * kMxBlocks * info->sm_count;
+        const int g = grid_for(n_blocks, many ? 4 * kMxBlocks : kMxBlocks, info);
+        auto kernel = many ? (vec ? dequantize_mxfp4_kernel<true, 4> : dequantize_mxfp4_kernel<false, 4>)
+                           : (vec ? dequantize_mxfp4_kernel<true, 1> : dequantize_mxfp4_kernel<false, 1>);
+        kernel<<<g, kQuantThreads, 0, s>>>(blocks, n_blocks, out);
         return cudaGetLastError();
     }
     const int grid = grid_for(n_elems, 256, info);
