@@ -1041,8 +1041,11 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         // in most cases; `groups` as if the pairs were spread by chance.
         const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
         const double mean = pairs / active;
-        const bool wide = mean > 6.0;
-        const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(active * std::max(1.0, mean / 16) + 0.5));
+        const bool wide = mean > 10.0;
+        const double per_group = wide ? 16.0 : 8.0;
+        // groups of Poisson-spread counts: about half a group more than full ones an expert
+        const int64_t groups = std::max<int64_t>(
+            1, static_cast<int64_t>(active * std::max(1.0, mean / per_group + 0.4) + 0.5));
         Params g{};
         g.W = m.W_gate;
         g.W2 = m.W_up;
