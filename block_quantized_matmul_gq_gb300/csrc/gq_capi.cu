@@ -122,16 +122,42 @@ cudaError_t internal_workspace(cudaStream_t s, size_t bytes, void** out) {
     return cudaSuccess;
 }
 
-// The same for the calls whose graphs would keep the buffer's address: they are refused while
-// the stream is being captured (the buffer can be freed by a later, larger call and is shared
-// by every call on the stream, which a replayed graph does not respect). Their _ws forms are
-// the ones to capture.
-cudaError_t eager_workspace(cudaStream_t s, size_t bytes, void** out) {
+// Workspace of the MXFP4 and expert calls without one of their own: a buffer per (device,
+// stream), apart from the one above. A call holds the lock until all its kernels are queued, so
+// that calls from several threads on one stream do not interleave in the buffer. Refused while
+// the stream is being captured: a graph would keep the address of a buffer that a later, larger
+// call frees, and that calls share in stream order, which replays do not respect. The _ws forms
+// are the ones to capture.
+struct CallSpace {
+    std::unique_lock<std::mutex> lock;
+    void* ptr = nullptr;
+};
+
+cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) {
+    static std::mutex mu;
+    static std::map<std::pair<int, void*>, std::pair<void*, size_t>> buffers;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    const cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    cudaError_t e = cudaStreamIsCapturing(s, &cap);
     if (e != cudaSuccess) return e;
     if (cap != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
-    return internal_workspace(s, bytes, out);
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::unique_lock<std::mutex> lock(mu);
+    auto& entry = buffers[std::make_pair(dev, static_cast<void*>(s))];
+    if (entry.second < bytes) {
+        e = cudaStreamSynchronize(s);   // the queued calls may still use the old buffer
+        if (e != cudaSuccess) return e;
+        if (entry.first) cudaFree(entry.first);
+        entry = {nullptr, 0};
+        void* p = nullptr;
+        e = cudaMalloc(&p, bytes);
+        if (e != cudaSuccess) return e;
+        entry = {p, bytes};
+    }
+    out->ptr = entry.first;
+    out->lock = std::move(lock);
+    return cudaSuccess;
 }
 
 // Runs one validated, non-empty problem (K > 0): tensor cores when the shape qualifies,
@@ -140,8 +166,10 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
                   cudaStream_t s) {
     if (t == GQ_TYPE_MXFP4) {
         const size_t need = static_cast<size_t>(gq::few_workspace_bytes(p.K, N));
+        CallSpace space;
         if (ws == nullptr) {
-            if (eager_workspace(s, need, &ws) != cudaSuccess) return GQ_ERR_CUDA;
+            if (call_space(s, need, &space) != cudaSuccess) return GQ_ERR_CUDA;
+            ws = space.ptr;
             ws_bytes = need;
         } else if (ws_bytes < need || !aligned(ws, 256)) {
             return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -312,11 +340,13 @@ gq_status plan_batch(const gq_mul_mat_problem* problems, int32_t count, gq_type 
 // one CUDA-core decode launch; all on `s`, all sharing workspace `ws` in stream order.
 gq_status run_batch(gq_type t, int64_t N, BatchPlan* plan, void* ws, size_t ws_bytes,
                     cudaStream_t s) {
+    CallSpace space;
     if (plan->ws_bytes > 0) {
         if (ws == nullptr) {
-            const cudaError_t e = t == GQ_TYPE_MXFP4 ? eager_workspace(s, plan->ws_bytes, &ws)
+            const cudaError_t e = t == GQ_TYPE_MXFP4 ? call_space(s, plan->ws_bytes, &space)
                                                      : internal_workspace(s, plan->ws_bytes, &ws);
             if (e != cudaSuccess) return GQ_ERR_CUDA;
+            if (t == GQ_TYPE_MXFP4) ws = space.ptr;
             ws_bytes = plan->ws_bytes;
         } else if (ws_bytes < plan->ws_bytes || !aligned(ws, 256)) {
             return ws_bytes < plan->ws_bytes ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -392,9 +422,11 @@ gq_status gq_mul_mat_rmsnorm(const void* W_blocks, gq_type t, int64_t M, int64_t
     const size_t xb = (static_cast<size_t>(N * K) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     void* w = nullptr;
-    if ((t == GQ_TYPE_MXFP4 ? eager_workspace(s, xb + down, &w)
+    CallSpace space;
+    if ((t == GQ_TYPE_MXFP4 ? call_space(s, xb + down, &space)
                             : internal_workspace(s, xb + down, &w)) != cudaSuccess)
         return GQ_ERR_CUDA;
+    if (t == GQ_TYPE_MXFP4) w = space.ptr;
     float* xhat = static_cast<float*>(w);
     cudaError_t e = gq::launch_rmsnorm_x(X, gamma, eps, N, K, xhat, s);
     if (e != cudaSuccess) return GQ_ERR_CUDA;
@@ -419,9 +451,11 @@ gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int
     const size_t yb = (static_cast<size_t>(N * M) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     void* w = nullptr;
-    if ((t == GQ_TYPE_MXFP4 ? eager_workspace(s, 2 * yb + down, &w)
+    CallSpace space;
+    if ((t == GQ_TYPE_MXFP4 ? call_space(s, 2 * yb + down, &space)
                             : internal_workspace(s, 2 * yb + down, &w)) != cudaSuccess)
         return GQ_ERR_CUDA;
+    if (t == GQ_TYPE_MXFP4) w = space.ptr;
     float* G = static_cast<float*>(w);
     float* U = reinterpret_cast<float*>(static_cast<uint8_t*>(w) + yb);
     void* dws = static_cast<uint8_t*>(w) + 2 * yb;
@@ -525,11 +559,11 @@ gq_status gq_mul_mat_mx4x(const void* W_blocks, gq_type t, int64_t M, int64_t K,
     if (st != GQ_OK || empty) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
-    void* w = nullptr;
-    if (eager_workspace(s, gq_mul_mat_mx4x_workspace_size(t, M, K, N), &w) != cudaSuccess)
+    CallSpace space;
+    if (call_space(s, gq_mul_mat_mx4x_workspace_size(t, M, K, N), &space) != cudaSuccess)
         return GQ_ERR_CUDA;
     const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
-    return from_cuda(gq::launch_mx4x(p, N, w, s));
+    return from_cuda(gq::launch_mx4x(p, N, space.ptr, s));
 }
 
 gq_status gq_moe_route(const float* logits, int64_t N, int64_t E, int32_t top_k, int32_t renorm,
@@ -547,6 +581,8 @@ gq_status gq_moe_route(const float* logits, int64_t N, int64_t E, int32_t top_k,
 
 namespace {
 
+constexpr int64_t kMaxWidth = int64_t(1) << 24;   // of an expert layer: 512 groups stay below 2^30 units
+
 // Checks a mixture-of-experts call; *run tells whether anything is to be computed.
 gq_status check_moe(const gq_moe_experts* x, const float* X, int64_t N, const int32_t* ids,
                     const float* weights, int32_t top_k, float* Y, gq::MoeProblem* m,
@@ -556,7 +592,7 @@ gq_status check_moe(const gq_moe_experts* x, const float* X, int64_t N, const in
     if (!known_type(x->type) || !known_type(x->down_type)) return GQ_ERR_TYPE;
     if (x->E < 1 || x->E > gq::kMoeMaxExperts || x->D < 1 || x->F < 1) return GQ_ERR_SHAPE;
     if (top_k < 1 || top_k > gq::kMoeMaxTopK) return GQ_ERR_SHAPE;
-    if (x->D > kMaxDim || x->F > kMaxDim || x->E * x->F > kMaxDim || x->E * x->D > kMaxDim)
+    if (x->D > kMaxWidth || x->F > kMaxWidth || x->E * x->F > kMaxDim || x->E * x->D > kMaxDim)
         return GQ_ERR_SHAPE;
     // both widths are a K of one product and the rows of another
     if (check_shape(x->type, x->E * x->F, x->D, N) != GQ_OK ||
@@ -614,10 +650,10 @@ gq_status gq_moe_swiglu(const gq_moe_experts* experts, const float* X, int64_t N
     const gq_status st = check_moe(experts, X, N, ids, weights, top_k, Y, &m, &run);
     if (st != GQ_OK || !run) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void* w = nullptr;
-    if (eager_workspace(s, static_cast<size_t>(gq::moe_workspace_bytes(m)), &w) != cudaSuccess)
+    CallSpace space;
+    if (call_space(s, static_cast<size_t>(gq::moe_workspace_bytes(m)), &space) != cudaSuccess)
         return GQ_ERR_CUDA;
-    return from_cuda(gq::launch_moe(m, w, s));
+    return from_cuda(gq::launch_moe(m, space.ptr, s));
 }
 
 gq_status gq_get_last_error(void* stream) {

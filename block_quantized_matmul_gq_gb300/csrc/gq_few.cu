@@ -387,9 +387,9 @@ struct Worker {
     __device__ __forceinline__ void issue() {
         if (fleft > 0) {
             const int l = lane & 3;
-            const int64_t chunk = fbyte + fc * (kCB * kBB);
+            const int64_t chunk = fbyte + static_cast<int64_t>(fc) * (kCB * kBB);
             const uint32_t dst = ring + fstage * kStageBytes + (lane >> 2) * kPitch + 16 * l;
-            if (ftile * 32 + 32 <= p.rows && chunk + 31 * p.row_bytes + 16 * kWords <= p.total_bytes) {
+            if (p.rows - ftile * 32 >= 32 && chunk + 31 * p.row_bytes + 16 * kWords <= p.total_bytes) {
                 int64_t at = chunk + (lane >> 2) * p.row_bytes;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -427,7 +427,7 @@ struct Worker {
         for (int j = 0; j < 4; ++j) {
             const int r = (M == kGateUp ? j & 1 : j) * 8 + (lane >> 2);
             const int64_t from = (chunk + r * p.row_bytes) & ~static_cast<int64_t>(15);
-            const int left = ftile * 32 + fs * 16 + r < p.rows
+            const int left = fs * 16 + r < p.rows - ftile * 32
                                  ? static_cast<int>(min(p.total_bytes - from, static_cast<int64_t>(16 * kWords))) : 0;
             const uint8_t* src = (M == kGateUp && j >= 2 ? p.W2 : p.W) + from;
 #pragma unroll 1
@@ -655,7 +655,7 @@ struct Worker {
                             float* out = p.out + row * p.rows + tile * 32 + g;
 #pragma unroll
                             for (int k = 0; k < 4; ++k)   // rows 8 k + g
-                                if (tile * 32 + 8 * k + g < p.rows) out[8 * k] = tot[k >> 1][n][2 * (k & 1) + i] * sc;
+                                if (8 * k + g < p.rows - tile * 32) out[8 * k] = tot[k >> 1][n][2 * (k & 1) + i] * sc;
                         }
                     }
             }
@@ -808,8 +808,9 @@ split_kernel(const float* __restrict__ X, int kb, int type, __half* __restrict__
 #pragma unroll 4
     for (int b = warp; b < kb; b += 16) {
         const Split s(x[b * 32 + lane], e);
-        out[b * 64] = s.hi;
-        out[b * 64 + 8] = s.lo;
+        __half* at = out + static_cast<int64_t>(b) * 64;
+        at[0] = s.hi;
+        at[8] = s.lo;
         if (type == GQ_TYPE_Q4_K) {
             float sum = s.sum();
 #pragma unroll
@@ -894,8 +895,8 @@ template <int T, int M, int Terms, int NT>
 cudaError_t launch_few(Params p, int64_t groups, const DeviceInfo* info, cudaStream_t s) {
     using Wk = Worker<T, M, Terms, NT>;
     p.chunks = (p.kb + Fmt<T>::cb - 1) / Fmt<T>::cb;
-    p.tiles = (p.rows + 31) / 32;
-    const int64_t units = p.tiles * groups;
+    p.tiles = static_cast<int>((static_cast<int64_t>(p.rows) + 31) / 32);
+    const int64_t units = static_cast<int64_t>(p.tiles) * groups;
     p.kshift = pick_kshift(units, p.chunks, 2 * info->sm_count * kWarps, NT == 1 ? 0.03 : 0.08);
     const int64_t rwarps = kWarps >> p.kshift;
     const unsigned grid = static_cast<unsigned>(

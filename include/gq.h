@@ -45,7 +45,10 @@
  *     before that call has completed. X and Y are touched only after it has completed, so
  *     one call's Y may be the next call's X, or the other way round. W_blocks must
  *     therefore not be memory that the immediately preceding libgq decode call on the
- *     stream writes (its Y); any other kernel in between orders the two calls as usual.
+ *     stream writes (its Y); any other kernel in between orders the two calls as usual. The
+ *     MXFP4 mul_mat, gq_mul_mat_mx4x and the gq_moe calls read nothing before everything ahead
+ *     of them on the stream has completed; like a decode call, they may let the next decode
+ *     call load its W_blocks before they have completed themselves.
  *     A prefill call (N >= 65) begins with an ordinary launch, so it starts only after
  *     everything before it on the stream has completed.
  *   - Errors. Argument checks run on the host before anything is launched and return a
@@ -176,17 +179,18 @@ gq_status gq_quantize_q4_k(const float* W, int64_t M, int64_t K, void* W_blocks,
  * into a graph (GQ_ERR_CUDA), the _ws forms and gq_mul_mat_noalloc do not. gq_mul_mat_batched
  * runs MXFP4 problems one after another. gq_mul_mat_rmsnorm and gq_mul_mat_swiglu take it in
  * their composite forms; gq_mul_mat_q8x does not (GQ_ERR_TYPE; gq_mul_mat_mx4x is its kind).
- * Range: where |X| / 2^e' of a block (e' as e above) and 2^(s - 127) are so far apart that a
- * product leaves fp32's normal range, it is rounded as fp32 is. Non-finite values of a token
- * reach that token's results alone.
+ * Range: X[n] is brought to a maximum in [2^14, 2^15) first, and sum_k What[m][k] X[n][k] in
+ * those units must stay inside fp32's range (it does for |What| below 2^80). max|X[n]| counts
+ * as at least 2^-110 in the bound. Non-finite values of a token reach that token's results
+ * alone, a block of scale 255 its weight row's.
  */
 gq_status gq_quantize_mxfp4(const float* W, int64_t M, int64_t K, void* W_blocks,
                             void* stream);
 
 /*
  * Expand blocks back to fp32: W_out[m][k] = (c - 8) * d (Q4_0), c * d (Q8_0),
- * 2^(s - 127) E2M1(c) (MXFP4), or d sc_j q - dmin m_j (Q4_K), exact up to Q4_K's one rounding ("Development Guide ...",
- * section 6.2, the unpack and dequantize steps). W_out receives M x K floats.
+ * 2^(s - 127) E2M1(c) (MXFP4), or d sc_j q - dmin m_j (Q4_K), exact up to Q4_K's one
+ * rounding ("Development Guide ...", section 6.2, the unpack and dequantize steps). W_out receives M x K floats.
  */
 gq_status gq_dequantize(const void* W_blocks, gq_type t, int64_t M, int64_t K,
                         float* W_out, void* stream);
@@ -372,7 +376,8 @@ gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int
  * (K / 32 + 160) 2^-24 sum_k |What[m][k] Xhat[n][k]|. With many
  * tokens it runs on the block-scaled tensor cores, which take MXFP4 operands as they are.
  * t must be GQ_TYPE_MXFP4 (else GQ_ERR_TYPE); other arguments as gq_mul_mat; any N. An X block
- * with an infinity or a NaN makes its token's results NaN.
+ * with an infinity or a NaN makes its token's results NaN. The product of two blocks' scales must
+ * be below 2^128; products below 2^-126 may be taken as zero.
  * gq_mul_mat_mx4x uses the library's workspace (refused while the stream is captured,
  * GQ_ERR_CUDA); gq_mul_mat_mx4x_ws the caller's: 256-byte aligned, at least
  * gq_mul_mat_mx4x_workspace_size bytes (0 for invalid or empty arguments), used by no other
@@ -420,14 +425,15 @@ typedef struct gq_moe_experts {
  *     the host during the call). Y must not overlap the other arrays.
  *   - An id outside [0, E) stands for no expert (padding): its weight is not read into the sum.
  *     A token without any gets Y[n] = 0. The same id twice counts twice.
- *   - D and F: multiples of 32, and of 256 where type (D) or down_type (F) is Q4_K; E <= 1024;
- *     1 <= top_k <= 64 (else GQ_ERR_SHAPE). Any N; N * top_k <= 512 runs in one pass over
- *     the chosen experts' weights (three launches), more in several.
+ *   - D and F: at most 2^24; multiples of 32, and of 256 where type (D) or down_type (F) is
+ *     Q4_K; E * D and E * F below 2^31; E <= 1024; 1 <= top_k <= 64 (else GQ_ERR_SHAPE). Any N; N * top_k <= 512 runs in one pass over
+ *     the chosen experts' weights (four launches), more in several.
  *   - Accuracy: fp32. X and the hidden vector are split in two fp16 terms (22 bits) and every
  *     sum is held in fp32: each product's error is at most (K / 32 + 160) 2^-24
  *     sum_k (|What| + |z|) |x| + 2^-38 max|x| sum_k (|What| + |z|), z = dmin m for Q4_K (0 for
  *     the other types), carried on as in gq_mul_mat_swiglu. Results are deterministic.
- *   - Only the weights of chosen experts are read, once per group of up to 16 tokens.
+ *   - Only the weights of chosen experts are read, once per group of up to 8 of an expert's
+ *     tokens (16 where the experts at work have more than ten on average).
  * Workspaces as for gq_mul_mat_mx4x: gq_moe_swiglu uses the library's (not in a capture),
  * gq_moe_swiglu_ws the caller's gq_moe_workspace_size bytes.
  */

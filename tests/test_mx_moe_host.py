@@ -86,6 +86,7 @@ def test_moe_refusals(gq_lib):
     assert call(type=12) == -2 and call(down_type=12) == -2          # D = 64, F = 96 under Q4_K
     assert call(k=0) == -2 and call(k=65) == -2 and call(N=-1) == -2
     assert call(E=1024, F=1 << 22) == -2                             # E * F rows too many
+    assert call(E=1, F=1 << 25) == -2 and call(E=1, D=1 << 25) == -2  # too wide
     for name in ("W_gate", "W_up", "W_down"):
         assert call(**{name: None}) == -1 and call(**{name: A8}) == -4
     for name in ("x", "ids", "w", "y"):
