@@ -344,16 +344,45 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
 
 // ---- Host side --------------------------------------------------------------------------
 
-constexpr int64_t kMxMinTokens = 17;   // below, the few-token kernel
+// Below, the few-token kernel. It reads the weights once for 8 or 16 tokens and prepares only X;
+// here all weights are laid out first. Both, in us for 8, 16 and 17 tokens (there, here):
+//   M x K 2048 x 2048     5.2  8.0    6.7  8.0    6.9  8.0
+//         5632 x 2048     7.4  9.2    9.4  9.2   13.3  9.2
+//        32000 x 2048    19.2 22.4   24.2 22.4   40.5 22.4
+//        11008 x 4096    18.8 18.8   23.4 18.8   34.1 18.8
+//         2048 x 5632     9.2 14.6   12.1 14.6   12.2 14.6
+constexpr int64_t kMxMinTokens = 17;
 
-int bn_for(int64_t N) { return N <= 64 ? 64 : (N <= 128 ? 128 : 192); }
+// Token columns of a tile: the fewest rounds of tiles over the SMs, of which a round costs a share
+// that does not depend on its columns (about 250 columns' worth), and the last one's results leave
+// with nothing beside them. In us with 64, 128 and 192 columns (tiles over 152 SMs in brackets):
+//   2048 x 2048, N = 512    9.0 (1)   9.9 (1)  11.2 (1)
+//   2048 x 2048, N = 2048  22.0 (4)  15.9 (2)  17.7 (2)
+//   5632 x 2048, N = 256   13.3 (2)  10.6 (1)  12.1 (1)
+//   5632 x 2048, N = 512   17.4 (3)  14.8 (2)  12.5 (1)
+//   11008 x 4096, N = 2048 148.9 (19) 91.0 (10) 78.6 (7)
+int bn_for(int64_t M, int64_t N) {
+    constexpr int64_t kSms = 152;   // a GB300's; the workspace's size is asked for without a device
+    const int64_t m_tiles = (M + kBM - 1) / kBM;
+    int best = 0;
+    int64_t least = 0;
+    for (int bn = 64; bn <= 192; bn += 64) {
+        const int64_t rounds = (m_tiles * ((N + bn - 1) / bn) + kSms - 1) / kSms;
+        const int64_t cost = rounds * (250 + bn) + bn;
+        if (best == 0 || cost < least) {
+            best = bn;
+            least = cost;
+        }
+    }
+    return best;
+}
 
 struct MxSpace {
     int64_t m_tiles, n_tiles, ktiles, w_bytes, x_bytes;
 };
 
 MxSpace mx_space(int64_t M, int64_t K, int64_t N) {
-    const int bn = bn_for(N);
+    const int bn = bn_for(M, N);
     MxSpace s{};
     s.m_tiles = (M + kBM - 1) / kBM;
     s.n_tiles = (N + bn - 1) / bn;
@@ -404,7 +433,7 @@ cudaError_t launch_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStr
     p.N = N;
     p.kb = static_cast<int>(m.K / 32);
     p.ktiles = static_cast<int>(at.ktiles);
-    p.bn = bn_for(N);
+    p.bn = bn_for(m.M, N);
     p.w_blocks = at.m_tiles * kBM * at.ktiles * kStageBlocks;
     p.x_blocks = at.n_tiles * p.bn * at.ktiles * kStageBlocks;
     const int64_t most = int64_t(info->sm_count) * 8;
