@@ -147,11 +147,6 @@ __device__ __forceinline__ void mma_next(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Byte i of w as fp32: 2^23 + byte under the exponent, less 2^23 (no conversion unit).
-__device__ __forceinline__ float byte_to_float(uint32_t w, int i) {
-    return __uint_as_float(__byte_perm(w, 0x4B000000u, i ? 0x7651 : 0x7650)) - 8388608.0f;
-}
-
 // Two E8M0 scale bytes to fp32 (255: NaN; 0: the subnormal 2^-127).
 __device__ __forceinline__ void e8m0_to_f32(uint32_t lo, uint32_t hi, float& dlo, float& dhi) {
     uint32_t r;
@@ -173,6 +168,11 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 constexpr uint32_t kMagic = 0x64006400u;       // 1024
@@ -207,18 +207,17 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
 template <int NT, int Terms>
 struct Columns {
     uint4 b[NT][Terms];        // eight fp16 of column g, hi and lo
-    float2 s[NT], sum[NT];     // scales and sums of tokens 2t, 2t + 1, where there are any
+    float2 s[NT];              // scales of tokens 2t, 2t + 1, where there are any per block
 };
 
-// Products of one 16-row tile with one block, for NT tiles of 8 tokens: tot += d_row s_token
-// (codes . columns), less m_row sum_token for Q4_K. tot: rows g, g + 8 x tokens 2t, 2t + 1.
-template <int T, int Terms, int NT, bool Scaled>
-__device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const float (&d)[2],
-                                               const float (&m)[2], const Columns<NT, Terms>& col,
-                                               float (&tot)[NT][4]) {
+// c = products of one 16-row tile with one block, for NT tiles of 8 tokens: rows g, g + 8 x tokens
+// 2t, 2t + 1.
+template <int Terms, int NT>
+__device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const Columns<NT, Terms>& col,
+                                               float (&c)[NT][4]) {
     // one column tile: hi and lo in chains of their own, to be added at the end
     constexpr bool kTwo = Terms == 2 && NT == 1;
-    float c[NT][4], l[4];
+    float l[4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][0].x, col.b[n][0].y);
@@ -238,15 +237,6 @@ __device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const 
         for (int n = 0; n < NT; ++n)
             mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][1].z, col.b[n][1].w);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = Scaled ? (i & 1 ? col.s[n].y : col.s[n].x) : 1.0f;
-            tot[n][i] = fmaf(Scaled ? d[i >> 1] * s : d[i >> 1], c[n][i], tot[n][i]);
-            if constexpr (T == GQ_TYPE_Q4_K)
-                tot[n][i] = fmaf(-m[i >> 1], i & 1 ? col.sum[n].y : col.sum[n].x, tot[n][i]);
-        }
 }
 
 // The shared lists of a launch over experts: pairs sorted by expert, and groups of pairs of one
@@ -440,7 +430,7 @@ struct Worker {
     struct Acts {
         const uint4* b[NT];
         const float* s[NT][2];
-        const float* sum[NT][2];
+        const float2* sum[NT];   // Q4_K: the sums of sub-blocks 2t, 2t + 1 for token g
     };
 
     // The block at hand, and on to the one `step` blocks later.
@@ -456,11 +446,6 @@ struct Worker {
                 c.s[n] = make_float2(*a.s[n][0], *a.s[n][1]);
                 a.s[n][0] += step;
                 a.s[n][1] += step;
-            }
-            if constexpr (kSums) {
-                c.sum[n] = make_float2(*a.sum[n][0], *a.sum[n][1]);
-                a.sum[n][0] += step;
-                a.sum[n][1] += step;
             }
         }
     }
@@ -493,7 +478,7 @@ struct Worker {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             uint32_t q[2][4];
-            float d[2], m[2] = {0.0f, 0.0f};
+            float d[2], c[NT][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (T == GQ_TYPE_Q8_0) {
@@ -511,40 +496,146 @@ struct Worker {
                 if constexpr (T != GQ_TYPE_MXFP4) d[h] = half_bits_to_float(x.d[mt][h]);
             }
             if constexpr (T == GQ_TYPE_MXFP4) e8m0_to_f32(x.d[mt][0], x.d[mt][1], d[0], d[1]);
-            block_products<T, Terms, NT, kScaled>(q, d, m, col, tot[mt]);
+            block_products<Terms, NT>(q, col, c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tot[mt][n][i] = fmaf(kScaled ? d[i >> 1] * (i & 1 ? col.s[n].y : col.s[n].x) : d[i >> 1],
+                                         c[n][i], tot[mt][n][i]);
         }
     }
 
-    // Q4_K: sub-blocks 2 j and 2 j + 1, which share code bytes (low and high nibbles).
-    __device__ __forceinline__ void pair_q4k(float (&tot)[2][NT][4], const uint32_t (&base)[2][2], int j,
-                                             const Cols& c0, const Cols& c1) const {
+    // Q4_K: the eight sub-blocks of a super-block, columns loaded ahead as in the other types.
+    //     sum_j (d sc_j sum q x - dmin m_j sum x) = d sum_j sum (sc_j q) x - dmin sum_j m_j X_j
+    // sc_j q, at most 63 x 15, is an exact fp16 integer and costs no instruction: codes under the
+    // exponent of 1024 become sc_j q by one multiply-add. So with one activation scale a row the
+    // products of a super-block chain in the accumulators; with one a sub-block (kDown) each
+    // sub-block's are added under its scale. The mins are one more product: m_j in k = j and
+    // k = 8 + j, with the two terms of the sub-blocks' sums X_j. (A scale and a min multiply-add
+    // for every sub-block, row and token: 56 instructions a sub-block and 16 rows instead of 35.)
+    __device__ __forceinline__ void super_block(float (&tot)[2][NT][4], const uint32_t (&base)[2][2],
+                                                Cols (&col)[kDepth], Acts& acts, int jump) const {
+        constexpr bool kTwo = NT == 1 && !kScaled;   // hi and lo in chains of their own
+        const int t = lane & 3;
+        float2 sums[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            sums[n] = *acts.sum[n];
+            acts.sum[n] += kwarps * (kCB / 2);
+        }
+        float acc[2][NT][4], low[2][4];
+#pragma unroll
+        for (int i = 0; i < kTotals; ++i) (&acc[0][0][0])[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) (&low[0][0])[i] = 0.0f;
+#pragma unroll 1
+        for (int b = 0; b < kCB; b += kDepth) {
+            const int step = (b + 2 * kDepth) % kCB ? 1 : jump;   // past a chunk's end
+            uint32_t scales[2][2];   // byte i: of sub-block b + i
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 hd = lds128(base[mt][h]);
+                    const uint32_t s = b & 4 ? (hd.w & 0x0F0F0F0Fu) | ((hd.y >> 2) & 0x30303030u) : hd.y & 0x3F3F3F3Fu;
+                    scales[mt][h] = kDepth == 4 ? s : s >> (8 * (b & 2));
+                }
+#pragma unroll
+            for (int i = 0; i < kDepth; i += 2) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t q[2][2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = base[mt][h] + 16 + 16 * (b + i) + 4 * t;
+                        const uint32_t w0 = lds32(at), w1 = lds32(at + 16), v0 = w0 >> 8, v1 = w1 >> 8;
+                        const uint32_t s0 = h2_sub(__byte_perm(scales[mt][h], 0x64u, 0x4040 | i * 0x101), kMagic);
+                        const uint32_t s1 = h2_sub(__byte_perm(scales[mt][h], 0x64u, 0x4040 | (i + 1) * 0x101), kMagic);
+                        // low nibbles: (1024 + q) s - 1024 s; high: (1024 + 16 q) s / 16 - 64 s
+                        const uint32_t z0 = h2_mul(s0, 0xE400E400u), f1 = h2_mul(s1, kSixteenth), z1 = h2_mul(s1, 0xD400D400u);
+                        q[0][h][0] = h2_fma((w0 & 0x000F000Fu) | kMagic, s0, z0);
+                        q[0][h][1] = h2_fma((v0 & 0x000F000Fu) | kMagic, s0, z0);
+                        q[0][h][2] = h2_fma((w1 & 0x000F000Fu) | kMagic, s0, z0);
+                        q[0][h][3] = h2_fma((v1 & 0x000F000Fu) | kMagic, s0, z0);
+                        q[1][h][0] = h2_fma((w0 & 0x00F000F0u) | kMagic, f1, z1);
+                        q[1][h][1] = h2_fma((v0 & 0x00F000F0u) | kMagic, f1, z1);
+                        q[1][h][2] = h2_fma((w1 & 0x00F000F0u) | kMagic, f1, z1);
+                        q[1][h][3] = h2_fma((v1 & 0x00F000F0u) | kMagic, f1, z1);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const Cols& x = col[i + k];
+                        if constexpr (kScaled) {
+                            float c[NT][4];
+                            block_products<Terms, NT>(q[k], x, c);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    acc[mt][n][r] = fmaf(r & 1 ? x.s[n].y : x.s[n].x, c[n][r], acc[mt][n][r]);
+                        } else {
+#pragma unroll
+                            for (int term = 0; term < 2; ++term)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    float(&to)[4] = kTwo && term ? low[mt] : acc[mt][n];
+                                    mma_next(to, q[k][0][0], q[k][1][0], q[k][0][1], q[k][1][1], x.b[n][term].x, x.b[n][term].y);
+                                    mma_next(to, q[k][0][2], q[k][1][2], q[k][0][3], q[k][1][3], x.b[n][term].z, x.b[n][term].w);
+                                }
+                        }
+                    }
+                }
+                load(col[i], acts, 1);
+                load(col[i + 1], acts, i + 2 < kDepth ? 1 : step);
+            }
+        }
+        // the sums in two terms: in units of 32 where the row has one scale (a sum is below 2^20),
+        // else in units of a power of two of the super-block
+        uint32_t hi[NT], lo[NT];
+        float2 unit[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f = 1.0f / 32.0f;
+            unit[n] = make_float2(32.0f, 32.0f);
+            if constexpr (kScaled) {
+                uint32_t most = max(__float_as_uint(sums[n].x) & 0x7FFFFFFFu, __float_as_uint(sums[n].y) & 0x7FFFFFFFu);
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                const int e = block_exponent(most);
+                const float u = pow2f(e - 14);   // of token g; the totals' tokens are 2t, 2t + 1
+                f = pow2f(14 - e);
+                unit[n] = make_float2(__shfl_sync(0xFFFFFFFFu, u, 8 * t), __shfl_sync(0xFFFFFFFFu, u, 8 * t + 4));
+            }
+            const float x = sums[n].x * f, y = sums[n].y * f;
+            const __half2 a = __floats2half2_rn(x, y);
+            const __half2 b = __floats2half2_rn(x - __low2float(a), y - __high2float(a));
+            hi[n] = reinterpret_cast<const uint32_t&>(a);
+            lo[n] = reinterpret_cast<const uint32_t&>(b);
+        }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            uint32_t q[2][2][4];
-            float d[2][2], m[2][2];
+            uint32_t m[2];
+            float d[2], dmin[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint4 hd = lds128(base[mt][h]);
-                const uint32_t at = base[mt][h] + 16 + 32 * j + 4 * (lane & 3);
-                const uint32_t w0 = lds32(at), w1 = lds32(at + 16), v0 = w0 >> 8, v1 = w1 >> 8;
-                q[0][h][0] = h2_sub((w0 & 0x000F000Fu) | kMagic, kMagic);
-                q[0][h][1] = h2_sub((v0 & 0x000F000Fu) | kMagic, kMagic);
-                q[0][h][2] = h2_sub((w1 & 0x000F000Fu) | kMagic, kMagic);
-                q[0][h][3] = h2_sub((v1 & 0x000F000Fu) | kMagic, kMagic);
-                q[1][h][0] = h2_fma((w0 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
-                q[1][h][1] = h2_fma((v0 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
-                q[1][h][2] = h2_fma((w1 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
-                q[1][h][3] = h2_fma((v1 & 0x00F000F0u) | kMagic, kSixteenth, 0xD400D400u);
-                uint32_t sc, mn;
-                q4k_scales(hd, j, sc, mn);
+                const uint32_t mins = t & 2 ? ((hd.w >> 4) & 0x0F0F0F0Fu) | ((hd.z >> 2) & 0x30303030u) : hd.z & 0x3F3F3F3Fu;
+                m[h] = h2_sub(__byte_perm(mins, 0x64u, t & 1 ? 0x4342 : 0x4140), kMagic);
+                d[h] = half_bits_to_float(hd.x);
+                dmin[h] = half_bits_to_float(hd.x >> 16);
+            }
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    d[s][h] = half_bits_to_float(hd.x) * byte_to_float(sc, s);
-                    m[s][h] = half_bits_to_float(hd.x >> 16) * byte_to_float(mn, s);
+            for (int n = 0; n < NT; ++n) {
+                float z[4];
+                mma_first(z, m[0], m[1], m[0], m[1], hi[n], lo[n]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float c = kTwo ? acc[mt][n][i] + low[mt][i] : acc[mt][n][i];
+                    tot[mt][n][i] = fmaf(d[i >> 1], c, tot[mt][n][i]);
+                    tot[mt][n][i] = fmaf(-dmin[i >> 1] * (i & 1 ? unit[n].y : unit[n].x), z[i], tot[mt][n][i]);
                 }
             }
-            block_products<T, Terms, NT, kScaled>(q[0], d[0], m[0], c0, tot[mt]);
-            block_products<T, Terms, NT, kScaled>(q[1], d[1], m[1], c1, tot[mt]);
         }
     }
 
@@ -567,8 +658,10 @@ struct Worker {
                     const int tok = 8 * n + 2 * t + i;
                     const int64_t at = static_cast<int64_t>(x_row(gi, tok < n_tok ? tok : 0)) * p.kb + wk * kCB;
                     if constexpr (kScaled) acts.s[n][i] = p.xs + at;
-                    if constexpr (kSums) acts.sum[n][i] = p.xsum + at;
                 }
+                if constexpr (kSums)
+                    acts.sum[n] = reinterpret_cast<const float2*>(
+                        p.xsum + static_cast<int64_t>(x_row(gi, 8 * n + g < n_tok ? 8 * n + g : 0)) * p.kb + wk * kCB + 2 * t);
             }
             float tot[2][NT][4];
 #pragma unroll
@@ -595,16 +688,7 @@ struct Worker {
                 // A column set is loaded again as soon as it has been used; codes are fetched a
                 // block ahead (behind the chunk: bytes of the stage that are not used).
                 if constexpr (T == GQ_TYPE_Q4_K) {
-#pragma unroll 1
-                    for (int b = 0; b < kCB; b += kDepth) {
-                        const int step = (b + 2 * kDepth) % kCB ? 1 : jump;   // past a chunk's end
-#pragma unroll
-                        for (int i = 0; i < kDepth; i += 2) {
-                            pair_q4k(tot, base, (b + i) >> 1, col[i], col[i + 1]);
-                            load(col[i], acts, 1);
-                            load(col[i + 1], acts, i + 2 < kDepth ? 1 : step);
-                        }
-                    }
+                    super_block(tot, base, col, acts, jump);
                 } else {
                     Raw raw[2];
                     fetch(raw[0], base, 0);
