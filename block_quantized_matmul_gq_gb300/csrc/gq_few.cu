@@ -54,7 +54,7 @@ struct Fmt<GQ_TYPE_Q4_0> {
 };
 template <>
 struct Fmt<GQ_TYPE_Q8_0> {
-    static constexpr int bb = kQ8Bytes, cb = 4, pitch = 176;
+    static constexpr int bb = kQ8Bytes, cb = 4, pitch = 160;
 };
 template <>
 struct Fmt<GQ_TYPE_Q4_K> {   // a super-block's bytes over its 8 sub-blocks
@@ -102,6 +102,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
@@ -215,21 +220,13 @@ struct Columns {
 template <int Terms, int NT>
 __device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const Columns<NT, Terms>& col,
                                                float (&c)[NT][4]) {
-    // one column tile: hi and lo in chains of their own, to be added at the end
-    constexpr bool kTwo = Terms == 2 && NT == 1;
-    float l[4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][0].x, col.b[n][0].y);
-    if constexpr (kTwo) mma_first(l, q[0][0], q[1][0], q[0][1], q[1][1], col.b[0][1].x, col.b[0][1].y);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][0].z, col.b[n][0].w);
-    if constexpr (kTwo) {
-        mma_next(l, q[0][2], q[1][2], q[0][3], q[1][3], col.b[0][1].z, col.b[0][1].w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[0][i] += l[i];
-    } else if constexpr (Terms == 2) {
+    if constexpr (Terms == 2) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             mma_next(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][1].x, col.b[n][1].y);
@@ -459,6 +456,24 @@ struct Worker {
     // of their places (eight rows are a multiple of 8 bytes): the aligned word before a code
     // word, and the shift that takes the word out of two.
     __device__ __forceinline__ void fetch(Raw& x, const uint32_t (&base)[2][2], int pos) const {
+        if constexpr (T == GQ_TYPE_Q8_0) {
+            // bytes 8t..8t+7: out of two aligned 8-byte words (a lane's four rows, 8 apart, agree
+            // in the low four bits of their places)
+            const uint32_t first = base[0][0] + pos + 2 + 8 * (lane & 3);
+            const bool odd = first & 4u;
+            const int off = static_cast<int>((first & ~7u) - base[0][0]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 a = lds64(base[mt][h] + off), b = lds64(base[mt][h] + off + 8);
+                    const uint32_t mid = odd ? b.x : a.y;
+                    x.w[mt][h][0] = __funnelshift_r(odd ? a.y : a.x, mid, first << 3);
+                    x.w[mt][h][1] = __funnelshift_r(mid, odd ? b.y : b.x, first << 3);
+                    x.d[mt][h] = lds16(base[mt][h] + pos);
+                }
+            return;
+        }
         constexpr int kHead = T == GQ_TYPE_MXFP4 ? 1 : 2;
         const uint32_t r = (base[0][0] + pos + kHead) & 3u;
         const int off = pos + kHead - static_cast<int>(r) + 4 * (lane & 3);
@@ -468,8 +483,6 @@ struct Worker {
             for (int h = 0; h < 2; ++h) {
                 const uint32_t at = base[mt][h] + off;
                 x.w[mt][h][0] = __funnelshift_r(lds32(at), lds32(at + 4), r << 3);
-                if constexpr (T == GQ_TYPE_Q8_0)
-                    x.w[mt][h][1] = __funnelshift_r(lds32(at + 16), lds32(at + 20), r << 3);
                 x.d[mt][h] = T == GQ_TYPE_MXFP4 ? lds8(base[mt][h] + pos) : lds16(base[mt][h] + pos);
             }
     }

@@ -29,12 +29,11 @@ namespace gq {
 // pairs in these orders. The contraction does not depend on the order, so activations are
 // stored in the weights' order and no weight is ever moved between lanes.
 __host__ __device__ __forceinline__ int few_place(int type, int i) {
+    if (type == GQ_TYPE_Q8_0) return i;                     // lane t: bytes 8t..8t+7
     const int t = (i & 15) >> 2, r = i & 3, hi = i >> 4;
     int slot;
     if (type == GQ_TYPE_MXFP4)
         slot = 2 * r + hi;                                  // byte r: (low, high) nibbles
-    else if (type == GQ_TYPE_Q8_0)
-        slot = r + 4 * hi;                                  // four bytes of each word
     else if (type == GQ_TYPE_Q4_0)
         slot = 2 * (2 * (r & 1) + hi) + (r >> 1);           // masks 0x000F000F << 0, 4, 8, 12
     else
