@@ -6,17 +6,23 @@
 // with xs = x / s split in two fp16 terms (gq_few.cuh). The inner sum runs on the tensor
 // cores: mma.m16n8k16 with 16 weight rows as exact fp16 codes and 8 tokens as columns, four
 // instructions a block (two halves of k, hi and lo into the same fp32 accumulators); the outer
-// sum is one fp32 multiply-add per block, row and token. Nothing is rounded below 22 bits but
-// the fp32 sums.
+// sum is one fp32 multiply-add per block, row and token (Q4_K: per super-block, see super_block).
+// Nothing is rounded below 22 bits but the fp32 sums.
 //
-// What bounds it. One pass over the weights: 17 to 34 bytes per 32 weights from DRAM, about 40
+// What bounds it. One pass over the weights: 17 to 34 bytes per 32 weights from DRAM, 35 to 55
 // instructions per 16 rows x 32 weights x 8 tokens. At 6.8 TB/s an SM takes in 512 4-bit weights
-// every 12 cycles, 47 issue slots, so instructions come before memory as the limit, and with
-// them the instruction cache: forms of this kernel with all loops unrolled (70 to 150 KB of
-// code) took 4 to 10 us for a stage that this one ends in one. Loops here stay rolled, what is
-// rare is not inlined, and the number of column tiles is the kernel's, not a branch's. tcgen05
-// is not used: its operands would have to pass through shared memory once more, the scales
-// would have to be applied outside, and its 128-row tiles leave most SMs without work here.
+// every 12 cycles, 48 issue slots, so with issue slots half filled instructions and the latencies
+// between them come before memory as the limit: 304 CTAs of 8 warps (128 registers) issue in 38 %
+// (Q8_0: the shared-memory queue) to 53 % (Q4_K) of the cycles, tensor cores are at 12 to 18 %,
+// DRAM at 20 to 35 %. Measured, as a graph on a GB300: 11008 x 4096 MXFP4 times 13 tokens is
+// 23.0 us (5.4 us of bytes), an expert layer of 16 tokens over 64 Q8_0 experts 98 us (38), of 61
+// tokens over 64 Q4_K experts 144 us (33), of 4 tokens over 16 of 32 MXFP4 experts 39 us (9).
+// Next to it the instruction cache: forms of this kernel with all loops unrolled (70 to 150 KB of
+// code) lost 4 to 10 us a launch, so loops stay rolled, what is rare is not inlined, and the number
+// of column tiles is the kernel's, not a branch's. tcgen05 is not used: its operands would have to
+// pass through shared memory once more, fp16 scales would have to be applied outside, and its
+// 128-row tiles leave most SMs without work here. (The microscaled product, whose scales the
+// tensor cores apply, does use it: gq_mx.cu.)
 //
 // Layout of the work. A unit is (a group of up to 8 NT tokens, 32 result rows); a row warp has a
 // run of consecutive units, so that those of one group follow each other and share activations
@@ -334,8 +340,9 @@ struct Worker {
     static constexpr bool kSums = T == GQ_TYPE_Q4_K;
     static constexpr int kSub = M == kGateUp ? 2 : 1;   // a unit's passes: 16 gate and 16 up rows each
     static constexpr int kTotals = 2 * NT * 4;   // a lane's, of one pass
-    // Blocks whose activations are in registers ahead of their use: an L2 access takes 600 cycles,
-    // a warp's block about 130.
+    // Blocks whose activations are in registers ahead of their use: they come from L1 or L2, and a
+    // warp, one of four on its scheduler, is at a block for some 130 to 250 cycles. Four fit the
+    // registers with one column tile, two with two.
     static constexpr int kDepth = NT == 1 ? 4 : 2;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kSumBytes = kWarps * kTotals * 32 * 4;
@@ -1136,7 +1143,8 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const MoeSpace at = moe_space(m, n);
         const int pairs = static_cast<int>(n * m.top_k);
         // One tile of 8 tokens, or two where an expert at work has more on average than fit one
-        // in most cases; `groups` as if the pairs were spread by chance.
+        // in most cases (61 tokens over 64 Q4_K experts, 7.6 pairs an expert: 144 us with one,
+        // 165 us with two); `groups` as if the pairs were spread by chance.
         const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
         const double mean = pairs / active;
         const bool wide = mean > 10.0;

@@ -12,15 +12,17 @@
 // 128 weight rows (kBN token rows) x 256 k, i.e. rows of 128 bytes in the 128-byte swizzle, then
 // the scales as 32-row x 16-byte atoms (row r's four scales at (r % 32) 16 + (r / 32) 4), so that
 // one bulk copy brings a stage's operand. X is quantized on the way. This costs the weights one
-// more read and write (about 0.3 us a MB); laid out inside the product it would be paid again
-// for every token tile, and would put warps between the copies and the MMA.
+// more read and write (15 us of 79 for 11008 x 4096 times 2048 tokens); laid out inside the
+// product it would be paid again for every token tile, and would put warps between the copies and
+// the MMA.
 //
 // mx_gemm_kernel: one persistent CTA per SM; one thread copies, one issues MMAs (four of K = 64
 // a stage, after the copies of the scales to TMEM), four warps read one accumulator out while
-// the other fills. What bounds it: the fp32 results. At M = 11008, K = 4096, N = 2048 the
-// operands are 29 MB, Y is 90 MB, and the products take 185 GFLOP. Tiles of 128 x 192 because
-// two accumulators of 192 columns and two sets of scales fit TMEM's 512 columns (256 would leave
-// no room to overlap); 44 KB a stage from L2.
+// the other fills. What bounds it: a stage's 44 KB from L2 for 128 x 192 x 256 products, and the
+// fp32 results. At M = 11008, K = 4096, N = 2048 it takes 64 us for 185 GFLOP: 0.6 GB over the
+// L2's ports, 90 MB of Y; the tensor cores, at 2900 TFLOP/s then, are busy 31 % of the time. The
+// whole call is 79 us, 2350 TFLOP/s. Tiles of 128 x 192 because two accumulators of 192 columns
+// and two sets of scales fit TMEM's 512 columns (256 would leave no room to overlap).
 #include <algorithm>
 #include <atomic>
 
@@ -71,91 +73,112 @@ struct PrepareParams {
     int kb, ktiles;      // blocks of a row; 256-k tiles
     int bn;
     int64_t w_ctas;      // CTAs that lay out weights; the others quantize X
-    int64_t w_blocks, x_blocks;   // padded blocks of either
+    int64_t w_units, x_units;
 };
 
-// Weights: one thread per 17-byte block. X: four lanes per block (lane q: elements 4q..4q+3 and
-// 16+4q..), as in the quantizer. Rows and k that pad a record are zeros with scale 2^0.
-__global__ void __launch_bounds__(256) mx_prepare_kernel(const __grid_constant__ PrepareParams p) {
+// Weights: one thread per 17-byte block, a unit is 32 Each rows of a record. X: four lanes per
+// block (lane q: elements 4q..4q+3 and 16+4q..), as in the quantizer, a unit is 8 Each rows. Rows
+// and k that pad a record are zeros with scale 2^0. What bounds it is the latency of the reads:
+// with Each = 4 four blocks a thread are on their way (one and four, whole products in us:
+// 32000 x 2048 times 17 tokens 21.7 and 20.2, 11008 x 4096 times 2048 80.7 and 77.4; but
+// 256 x 2048 times 64, where CTAs are few, 7.4 and 8.1).
+template <int Each>
+__global__ void __launch_bounds__(256, 4) mx_prepare_kernel(const __grid_constant__ PrepareParams p) {
     griddep_wait();   // X, and the records that a product before may still read
     griddep_launch_dependents();
-    const int kpad = p.ktiles * kStageBlocks;
+    const unsigned ktiles = static_cast<unsigned>(p.ktiles);
     if (blockIdx.x < p.w_ctas) {
+        constexpr unsigned kParts = kBM / 32 / Each;   // units of a record
         const int64_t total = p.M * p.kb * kMxfp4Bytes;
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.w_blocks;
-             i += p.w_ctas * 256) {
-            const int64_t row = i / kpad;
-            const int kb = static_cast<int>(i - row * kpad);
-            uint4 codes = make_uint4(0u, 0u, 0u, 0u);
-            uint32_t scale = 127;
-            if (row < p.M && kb < p.kb) {
-                const int64_t at = (row * p.kb + kb) * kMxfp4Bytes, from = at & ~int64_t(3);
-                uint32_t w[6];
+        const int j = threadIdx.x & 7;
+        for (int64_t u = blockIdx.x; u < p.w_units; u += p.w_ctas) {
+            const unsigned record = static_cast<unsigned>(u) / kParts, tile = record / ktiles, k = record - tile * ktiles;
+            const int r0 = static_cast<int>(static_cast<unsigned>(u) % kParts) * (32 * Each) + (threadIdx.x >> 3);
+            const int64_t row0 = static_cast<int64_t>(tile) * kBM + r0;
+            const int kb = static_cast<int>(k) * kStageBlocks + j;
+            uint32_t w[Each][5], lead[Each];
 #pragma unroll
-                for (int k = 0; k < 5; ++k) {
-                    if (from + 4 * k + 4 <= total) {
-                        w[k] = *reinterpret_cast<const uint32_t*>(p.W + from + 4 * k);
-                    } else {   // the matrix ends inside this word
-                        w[k] = 0;
-                        for (int b = 0; b < 4; ++b)
-                            if (from + 4 * k + b < total) w[k] |= uint32_t(p.W[from + 4 * k + b]) << (8 * b);
+            for (int e = 0; e < Each; ++e) {
+                const int64_t row = row0 + 32 * e, at = (row * p.kb + kb) * kMxfp4Bytes, from = at & ~int64_t(3);
+                const bool real = row < p.M && kb < p.kb;
+                lead[e] = real ? static_cast<uint32_t>(at - from) : 4u;
+                if (real && from + 20 <= total) {
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) w[e][i] = *reinterpret_cast<const uint32_t*>(p.W + from + 4 * i);
+                } else {   // the matrix ends inside these words
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) {
+                        w[e][i] = 0;
+                        if (real)
+                            for (int b = 0; b < 4; ++b)
+                                if (from + 4 * i + b < total) w[e][i] |= uint32_t(p.W[from + 4 * i + b]) << (8 * b);
                     }
                 }
-                w[5] = 0;
-                // bytes 1..16 of the block: `sh` bits into the words
-                const uint32_t lead = static_cast<uint32_t>(at - from);
-                scale = (w[0] >> (8 * lead)) & 0xFFu;
-                const uint32_t sh = 8 * (lead + 1);
-                if (sh == 32) {
-                    codes = make_uint4(w[1], w[2], w[3], w[4]);
-                } else {
-                    codes = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-                }
             }
-            const int r = static_cast<int>(row & (kBM - 1)), j = kb & 7;
-            uint8_t* rec = p.wrec + ((row >> 7) * p.ktiles + (kb >> 3)) * static_cast<int64_t>(record_bytes(kBM));
-            *reinterpret_cast<uint4*>(rec + code_at(r, j)) = codes;
-            rec[scale_at(kBM, r, j)] = static_cast<uint8_t>(scale);
+            uint8_t* rec = p.wrec + static_cast<int64_t>(record) * record_bytes(kBM);
+#pragma unroll
+            for (int e = 0; e < Each; ++e) {
+                // byte 0 of the block `lead` bytes into the words, bytes 1..16 behind it
+                uint4 codes = make_uint4(w[e][1], w[e][2], w[e][3], w[e][4]);
+                uint32_t scale = w[e][0] >> 24;
+                if (lead[e] < 3) {
+                    const uint32_t sh = 8 * (lead[e] + 1);
+                    scale = (w[e][0] >> (8 * lead[e])) & 0xFFu;
+                    codes = make_uint4(__funnelshift_r(w[e][0], w[e][1], sh), __funnelshift_r(w[e][1], w[e][2], sh),
+                                       __funnelshift_r(w[e][2], w[e][3], sh), __funnelshift_r(w[e][3], w[e][4], sh));
+                }
+                const int r = r0 + 32 * e;
+                *reinterpret_cast<uint4*>(rec + code_at(r, j)) = codes;   // padding: all zeros
+                rec[scale_at(kBM, r, j)] = static_cast<uint8_t>(lead[e] == 4 ? 127u : scale);
+            }
         }
         return;
     }
-    const int q = threadIdx.x & 3;
-    const int64_t x_ctas = gridDim.x - p.w_ctas;
-    const int64_t steps = (p.x_blocks + 63) / 64;
-    for (int64_t s = blockIdx.x - p.w_ctas; s < steps; s += x_ctas) {
-        const int64_t i = s * 64 + (threadIdx.x >> 2);
-        const int64_t row = i / kpad;
-        const int kb = static_cast<int>(i - row * kpad);
-        const bool real = i < p.x_blocks && row < p.N && kb < p.kb;
-        float v[8] = {};
-        if (real) {
-            const float* src = p.X + (row * p.kb + kb) * 32 + 4 * q;   // only 4-byte aligned
-            if ((reinterpret_cast<uintptr_t>(p.X) & 15) == 0) {
-                const float4 a = *reinterpret_cast<const float4*>(src);
-                const float4 b = *reinterpret_cast<const float4*>(src + 16);
-                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            } else {
+    const int q = threadIdx.x & 3, j = (threadIdx.x >> 2) & 7;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.X) & 15) == 0;
+    const unsigned parts = static_cast<unsigned>(p.bn) / (8 * Each);   // units of a record
+    for (int64_t u = blockIdx.x - p.w_ctas; u < p.x_units; u += gridDim.x - p.w_ctas) {
+        const unsigned record = static_cast<unsigned>(u) / parts, part = static_cast<unsigned>(u) - record * parts;
+        const unsigned tile = record / ktiles, k = record - tile * ktiles;
+        const int kb = static_cast<int>(k) * kStageBlocks + j;
+        const int r0 = static_cast<int>(part) * (8 * Each) + (threadIdx.x >> 5);
+        const int64_t row0 = static_cast<int64_t>(tile) * p.bn + r0;
+        uint8_t* rec = p.xrec + static_cast<int64_t>(record) * record_bytes(p.bn);
+        float v[Each][8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k] = src[k];
-                    v[4 + k] = src[16 + k];
+        for (int e = 0; e < Each; ++e) {
+            const float* src = p.X + ((row0 + 8 * e) * p.kb + kb) * 32 + 4 * q;   // only 4-byte aligned
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[e][i] = 0.0f;
+            if (row0 + 8 * e < p.N && kb < p.kb) {
+                if (vec) {
+                    const float4 a = *reinterpret_cast<const float4*>(src);
+                    const float4 b = *reinterpret_cast<const float4*>(src + 16);
+                    v[e][0] = a.x; v[e][1] = a.y; v[e][2] = a.z; v[e][3] = a.w;
+                    v[e][4] = b.x; v[e][5] = b.y; v[e][6] = b.z; v[e][7] = b.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[e][i] = src[i];
+                        v[e][4 + i] = src[16 + i];
+                    }
                 }
             }
         }
-        uint32_t amax = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        if (i >= p.x_blocks) continue;
-        const uint32_t byte = real ? mx_scale_byte(amax) : 127u;
-        const uint32_t codes = real && byte != 255 ? mx_codes(v, mx_inverse_scale(byte)) : 0u;
-        const int tile = static_cast<int>(row / p.bn), r = static_cast<int>(row - int64_t(tile) * p.bn), j = kb & 7;
-        uint8_t* rec = p.xrec + (static_cast<int64_t>(tile) * p.ktiles + (kb >> 3)) * record_bytes(p.bn);
-        *reinterpret_cast<uint32_t*>(rec + code_at(r, j) + 4 * q) = codes;
-        if (q == 0) rec[scale_at(p.bn, r, j)] = static_cast<uint8_t>(byte);
+        for (int e = 0; e < Each; ++e) {
+            const int r = r0 + 8 * e;
+            const bool real = row0 + 8 * e < p.N && kb < p.kb;
+            uint32_t amax = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[e][i]) & 0x7FFFFFFFu);
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const uint32_t byte = real ? mx_scale_byte(amax) : 127u;
+            const uint32_t codes = real && byte != 255 ? mx_codes(v[e], mx_inverse_scale(byte)) : 0u;
+            *reinterpret_cast<uint32_t*>(rec + code_at(r, j) + 4 * q) = codes;
+            if (q == 0) rec[scale_at(p.bn, r, j)] = static_cast<uint8_t>(byte);
+        }
     }
 }
 
@@ -346,11 +369,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
 
 // Below, the few-token kernel. It reads the weights once for 8 or 16 tokens and prepares only X;
 // here all weights are laid out first. Both, in us for 8, 16 and 17 tokens (there, here):
-//   M x K 2048 x 2048     5.2  8.0    6.7  8.0    6.9  8.0
-//         5632 x 2048     7.4  9.2    9.4  9.2   13.3  9.2
-//        32000 x 2048    19.2 22.4   24.2 22.4   40.5 22.4
-//        11008 x 4096    18.8 18.8   23.4 18.8   34.1 18.8
-//         2048 x 5632     9.2 14.6   12.1 14.6   12.2 14.6
+//   M x K 2048 x 2048     5.2  7.6    6.7  7.6    6.9  7.6
+//         5632 x 2048     7.4  8.8    9.4  8.8   13.3  8.8
+//        32000 x 2048    19.2 20.2   24.2 20.2   40.5 20.2
+//        11008 x 4096    18.8 17.2   23.4 17.2   34.1 17.2
+//         2048 x 5632     9.2 14.4   12.1 14.4   12.2 14.4
 constexpr int64_t kMxMinTokens = 17;
 
 // Token columns of a tile: the fewest rounds of tiles over the SMs, of which a round costs a share
@@ -422,7 +445,7 @@ cudaError_t launch_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStr
     cudaError_t e = current_device_info(&info);
     if (e != cudaSuccess) return e;
     const MxSpace at = mx_space(m.M, m.K, N);
-    if (at.m_tiles > 0x7FFFFFFF || at.n_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (at.m_tiles * at.ktiles > 0x07FFFFFF || at.n_tiles * at.ktiles > 0x07FFFFFF) return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PrepareParams p{};
     p.W = m.W;
@@ -434,12 +457,15 @@ cudaError_t launch_mx4x(const MatProblem& m, int64_t N, void* workspace, cudaStr
     p.kb = static_cast<int>(m.K / 32);
     p.ktiles = static_cast<int>(at.ktiles);
     p.bn = bn_for(m.M, N);
-    p.w_blocks = at.m_tiles * kBM * at.ktiles * kStageBlocks;
-    p.x_blocks = at.n_tiles * p.bn * at.ktiles * kStageBlocks;
+    // four blocks a thread where that leaves every SM its four CTAs
+    const int64_t w4 = at.m_tiles * at.ktiles * (kBM / 128), x4 = at.n_tiles * at.ktiles * (p.bn / 32);
     const int64_t most = int64_t(info->sm_count) * 8;
-    p.w_ctas = std::min<int64_t>((p.w_blocks + 255) / 256, most);
-    const int64_t x_ctas = std::min<int64_t>((p.x_blocks + 63) / 64, most);
-    e = launch_after(mx_prepare_kernel, dim3(static_cast<unsigned>(p.w_ctas + x_ctas)), 256, 0, s, p);
+    const int each = w4 + x4 >= info->sm_count * 4 ? 4 : 1;
+    p.w_units = w4 * (4 / each);
+    p.x_units = x4 * (4 / each);
+    p.w_ctas = std::min(p.w_units, most);
+    const unsigned grid = static_cast<unsigned>(p.w_ctas + std::min(p.x_units, most));
+    e = launch_after(each == 4 ? mx_prepare_kernel<4> : mx_prepare_kernel<1>, dim3(grid), 256, 0, s, p);
     if (e != cudaSuccess) return e;
     const GemmParams g{p.wrec, p.xrec, m.Y, m.M, N, p.ktiles, static_cast<int>(at.m_tiles),
                        static_cast<int>(at.n_tiles), info->status};
