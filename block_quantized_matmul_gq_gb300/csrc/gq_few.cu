@@ -16,7 +16,7 @@
 // (Q8_0: the shared-memory queue) to 53 % (Q4_K) of the cycles, tensor cores are at 12 to 18 %,
 // DRAM at 20 to 35 %. Measured, as a graph on a GB300: 11008 x 4096 MXFP4 times 13 tokens is
 // 23.0 us (5.4 us of bytes), an expert layer of 16 tokens over 64 Q8_0 experts 98 us (38), of 61
-// tokens over 64 Q4_K experts 144 us (33), of 4 tokens over 16 of 32 MXFP4 experts 39 us (9).
+// tokens over 64 Q4_K experts 148 us (33), of 4 tokens over 16 of 32 MXFP4 experts 39 us (9).
 // Next to it the instruction cache: forms of this kernel with all loops unrolled (70 to 150 KB of
 // code) lost 4 to 10 us a launch, so loops stay rolled, what is rare is not inlined, and the number
 // of column tiles is the kernel's, not a branch's. tcgen05 is not used: its operands would have to
@@ -221,24 +221,34 @@ struct Columns {
     float2 s[NT];              // scales of tokens 2t, 2t + 1, where there are any per block
 };
 
-// c = products of one 16-row tile with one block, for NT tiles of 8 tokens: rows g, g + 8 x tokens
-// 2t, 2t + 1.
+// c (+)= products of one 16-row tile with one term of one block's activations, for NT tiles of 8
+// tokens: rows g, g + 8 x tokens 2t, 2t + 1.
+template <bool First, int Terms, int NT>
+__device__ __forceinline__ void term_products(const uint32_t (&q)[2][4], const Columns<NT, Terms>& col, int term,
+                                              float (&c)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (First)
+            mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][term].x, col.b[n][term].y);
+        else
+            mma_next(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][term].x, col.b[n][term].y);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][term].z, col.b[n][term].w);
+}
+
+// Both terms, the small one first: the tensor cores cut a sum off below the last bit of its
+// largest part (they do not round it), which costs the more the more often a sum of full size
+// passes through them.
 template <int Terms, int NT>
 __device__ __forceinline__ void block_products(const uint32_t (&q)[2][4], const Columns<NT, Terms>& col,
                                                float (&c)[NT][4]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        mma_first(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][0].x, col.b[n][0].y);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][0].z, col.b[n][0].w);
     if constexpr (Terms == 2) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            mma_next(c[n], q[0][0], q[1][0], q[0][1], q[1][1], col.b[n][1].x, col.b[n][1].y);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            mma_next(c[n], q[0][2], q[1][2], q[0][3], q[1][3], col.b[n][1].z, col.b[n][1].w);
+        term_products<true>(q, col, 1, c);
+        term_products<false>(q, col, 0, c);
+    } else {
+        term_products<true>(q, col, 0, c);
     }
 }
 
@@ -530,13 +540,14 @@ struct Worker {
     //     sum_j (d sc_j sum q x - dmin m_j sum x) = d sum_j sum (sc_j q) x - dmin sum_j m_j X_j
     // sc_j q, at most 63 x 15, is an exact fp16 integer and costs no instruction: codes under the
     // exponent of 1024 become sc_j q by one multiply-add. So with one activation scale a row the
-    // products of a super-block chain in the accumulators; with one a sub-block (kDown) each
-    // sub-block's are added under its scale. The mins are one more product: m_j in k = j and
-    // k = 8 + j, with the two terms of the sub-blocks' sums X_j. (A scale and a min multiply-add
-    // for every sub-block, row and token: 56 instructions a sub-block and 16 rows instead of 35.)
+    // products of two sub-blocks chain in the accumulators and add to the super-block's; with one a
+    // sub-block (kDown) each sub-block's are added under its scale. (Chains of all eight: 1.3e-6
+    // off in 61 tokens over 64 experts against 5e-7, at 144 us against 148.) The mins are one more
+    // product: m_j in k = j and k = 8 + j, with the two terms of the sub-blocks' sums X_j. (A scale
+    // and a min multiply-add for every sub-block, row and token: 56 instructions a sub-block and 16
+    // rows instead of 37, 173 us.)
     __device__ __forceinline__ void super_block(float (&tot)[2][NT][4], const uint32_t (&base)[2][2],
                                                 Cols (&col)[kDepth], Acts& acts, int jump) const {
-        constexpr bool kTwo = NT == 1 && !kScaled;   // hi and lo in chains of their own
         const int t = lane & 3;
         float2 sums[NT];
 #pragma unroll
@@ -544,11 +555,9 @@ struct Worker {
             sums[n] = *acts.sum[n];
             acts.sum[n] += kwarps * (kCB / 2);
         }
-        float acc[2][NT][4], low[2][4];
+        float acc[2][NT][4];
 #pragma unroll
         for (int i = 0; i < kTotals; ++i) (&acc[0][0][0])[i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) (&low[0][0])[i] = 0.0f;
 #pragma unroll 1
         for (int b = 0; b < kCB; b += kDepth) {
             const int step = (b + 2 * kDepth) % kCB ? 1 : jump;   // past a chunk's end
@@ -583,27 +592,27 @@ struct Worker {
                         q[1][h][2] = h2_fma((w1 & 0x00F000F0u) | kMagic, f1, z1);
                         q[1][h][3] = h2_fma((v1 & 0x00F000F0u) | kMagic, f1, z1);
                     }
+                    float c[NT][4];
+                    if constexpr (kScaled) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const Cols& x = col[i + k];
-                        if constexpr (kScaled) {
-                            float c[NT][4];
+                        for (int k = 0; k < 2; ++k) {
+                            const Cols& x = col[i + k];
                             block_products<Terms, NT>(q[k], x, c);
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
                                     acc[mt][n][r] = fmaf(r & 1 ? x.s[n].y : x.s[n].x, c[n][r], acc[mt][n][r]);
-                        } else {
-#pragma unroll
-                            for (int term = 0; term < 2; ++term)
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    float(&to)[4] = kTwo && term ? low[mt] : acc[mt][n];
-                                    mma_next(to, q[k][0][0], q[k][1][0], q[k][0][1], q[k][1][1], x.b[n][term].x, x.b[n][term].y);
-                                    mma_next(to, q[k][0][2], q[k][1][2], q[k][0][3], q[k][1][3], x.b[n][term].z, x.b[n][term].w);
-                                }
                         }
+                    } else {
+                        term_products<true>(q[0], col[i], 1, c);
+                        term_products<false>(q[1], col[i + 1], 1, c);
+                        term_products<false>(q[0], col[i], 0, c);
+                        term_products<false>(q[1], col[i + 1], 0, c);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[mt][n][r] += c[n][r];
                     }
                 }
                 load(col[i], acts, 1);
@@ -651,8 +660,7 @@ struct Worker {
                 mma_first(z, m[0], m[1], m[0], m[1], hi[n], lo[n]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float c = kTwo ? acc[mt][n][i] + low[mt][i] : acc[mt][n][i];
-                    tot[mt][n][i] = fmaf(d[i >> 1], c, tot[mt][n][i]);
+                    tot[mt][n][i] = fmaf(d[i >> 1], acc[mt][n][i], tot[mt][n][i]);
                     tot[mt][n][i] = fmaf(-dmin[i >> 1] * (i & 1 ? unit[n].y : unit[n].x), z[i], tot[mt][n][i]);
                 }
             }
