@@ -1,4 +1,4 @@
-"""block_quantized_matmul_gq_gb300 -- block-quantized (Q4_0 / Q8_0) mul_mat for GB300.
+"""block_quantized_matmul_gq_gb300 -- block-quantized (Q4_0 / Q8_0 / Q4_K / MXFP4) mul_mat for GB300.
 
 The compute path is the C-ABI library ``libgq.so`` (hand-written sm_103a kernels, declared
 in ``include/gq.h``); ``binding`` is its thin Python face and loads the library on import,

@@ -984,10 +984,11 @@ void use_split(Params& p, const uint8_t* ws, const SplitSpace& at) {
 }
 
 // log2 of the warps that split a unit's K. Every row warp takes the same number of units but for
-// one, so the split that leaves the fewest warps idle wins, less what a join costs: at 8 tokens a
-// unit 3 % a doubling (16 tokens over 64 Q8_0 experts: 1210 units, 103, 105 and 113 us with 2, 4
-// and 8 warps that all have work), at 16 tokens 8 % (61 over 64 Q4_K experts: 177, 181, 186 and
-// 198 us with 1, 2, 4 and 8 warps).
+// one, so the split that leaves the fewest warps idle wins, less what a join costs: 3 % a doubling
+// at 8 tokens a unit, 8 % at 16. With 1, 2, 4 and 8 warps throughout, in us: 16 tokens over 64 Q8_0
+// experts 154, 99, 104, 111; 61 over 64 Q4_K experts 167, 147, 153, 170; 4 over 16 of 32 MXFP4
+// experts 64, 41, 39, 42 (all 8 tokens a unit); 11008 x 4096 MXFP4 times 13 tokens 28.7, 23.1, 24.1,
+// 27.3 (16 a unit).
 int pick_kshift(int64_t units, int chunks, int warps, double join) {
     int best = 0;
     double most = -1.0;
@@ -1151,8 +1152,8 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const MoeSpace at = moe_space(m, n);
         const int pairs = static_cast<int>(n * m.top_k);
         // One tile of 8 tokens, or two where an expert at work has more on average than fit one
-        // in most cases (61 tokens over 64 Q4_K experts, 7.6 pairs an expert: 144 us with one,
-        // 165 us with two); `groups` as if the pairs were spread by chance.
+        // in most cases (61 tokens over 64 Q4_K experts, 7.6 pairs an expert: 147 us with one,
+        // 167 us with two); `groups` as if the pairs were spread by chance.
         const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
         const double mean = pairs / active;
         const bool wide = mean > 10.0;
