@@ -37,7 +37,7 @@ constexpr int kStageK = 256;      // k of a stage: 128 bytes a row
 constexpr int kStageBlocks = kStageK / 32;
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kAtom = 512;        // scales of 128 rows x 4 blocks
-constexpr int kMxThreads = 192;   // producer warp, MMA warp, four epilogue warps
+constexpr int kMxThreads = 320;   // producer warp, MMA warp, four epilogue warps, four scale warps
 
 __host__ __device__ constexpr int chunks_of(int rows) { return (rows + 127) / 128; }
 // Bytes of an operand record of `rows` rows: codes, then for each four blocks the atoms.
@@ -49,10 +49,10 @@ struct Mx {
     static constexpr int kStage = kA + kB;
     static constexpr int kStages = 5;
     static constexpr int kSmem = kStages * kStage + 1024;   // stages on 1024-byte boundaries
-    // TMEM columns: two accumulators, then two sets of scales (8 for A, 8 or 16 for B)
+    // TMEM columns: two accumulators, then a set of scales for each stage (8 for A, 8 or 16 for B)
     static constexpr int kScales = 2 * BN, kScaleSet = 8 + 8 * chunks_of(BN);
-    static constexpr int kColumns = 2 * BN + 2 * kScaleSet <= 256 ? 256 : 512;
-    static_assert(2 * BN + 2 * kScaleSet <= 512 && kStage % 1024 == 0 && kA % 1024 == 0, "layout");
+    static constexpr int kUsed = 2 * BN + kStages * kScaleSet, kColumns = kUsed <= 256 ? 256 : 512;
+    static_assert(kUsed <= 512 && kStage % 1024 == 0 && kA % 1024 == 0, "layout");
 };
 
 // ---- Preparation ------------------------------------------------------------------------
@@ -202,12 +202,15 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
-// One atom of scales (32 rows x 16 bytes, 8-row groups 128 bytes apart, no swizzle) to four TMEM
-// columns, repeated in the four 32-lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
-                          (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// Eight TMEM columns of a warp's 32 lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t* r) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 
 struct GemmParams {
@@ -223,7 +226,7 @@ template <int BN>
 __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_constant__ GemmParams p) {
     using C = Mx<BN>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], scaled[C::kStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_at;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_addr(&full[i]), 1);
             mbar_init(smem_addr(&empty[i]), 1);
+            mbar_init(smem_addr(&scaled[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&acc_full[i]), 1);
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
     } else if (warp == 1) {
         if (lane == 0) {
             int slot = 0, n_tile = 0;
-            uint32_t phase = 0, set = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n_tile) {
                 const int buf = n_tile & 1;
@@ -296,26 +300,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
                 for (int k = 0; k < p.ktiles; ++k) {
-                    ok = mbar_wait(smem_addr(&full[slot]), phase);
+                    ok = mbar_wait(smem_addr(&full[slot]), phase) && mbar_wait(smem_addr(&scaled[slot]), phase);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t a = ring + slot * C::kStage, b = a + C::kA;
-                    const uint32_t sfa = tmem + C::kScales + set * C::kScaleSet, sfb = sfa + 8;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        copy_scales(sfa + 4 * g, a + kBM * kRowBytes + g * kAtom);
-#pragma unroll
-                        for (int c = 0; c < chunks_of(BN); ++c)
-                            copy_scales(sfb + 4 * (chunks_of(BN) * g + c),
-                                        b + BN * kRowBytes + (chunks_of(BN) * g + c) * kAtom);
-                    }
+                    const uint32_t sfa = tmem + C::kScales + slot * C::kScaleSet, sfb = sfa + 8;
                     const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(b);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)   // 32 bytes of a row each
                         umma_mxf4(d, ad + 2 * i, bd + 2 * i, i & 1 ? mx_idesc(kBM, BN, 2) : mx_idesc(kBM, BN, 0),
                                   sfa + 4 * (i >> 1), sfb + 4 * chunks_of(BN) * (i >> 1), k > 0 || i > 0);
                     umma_commit(smem_addr(&empty[slot]));
-                    set ^= 1;
                     if (++slot == C::kStages) {
                         slot = 0;
                         phase ^= 1;
@@ -327,6 +322,41 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
             umma_commit(smem_addr(&drained));   // nothing may run when TMEM is given back
             mbar_wait(smem_addr(&drained), 0);
         }
+    } else if (warp >= 6) {
+        // scales: the same 32 rows of every atom into each quarter of the TMEM lanes
+        constexpr int kB = chunks_of(BN);
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int k = 0; k < p.ktiles; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&full[slot]), phase));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = ring + slot * C::kStage + kBM * kRowBytes + lane * 16;
+                const uint32_t b = ring + slot * C::kStage + C::kA + BN * kRowBytes + lane * 16;
+                const uint32_t to = tmem + C::kScales + slot * C::kScaleSet + (static_cast<uint32_t>(warp & 3) << 21);
+                uint32_t r[8 + 8 * kB];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) lds128(a + i * kAtom, r + 4 * i);
+#pragma unroll
+                for (int i = 0; i < 2 * kB; ++i) lds128(b + i * kAtom, r + 8 + 4 * i);
+#pragma unroll
+                for (int i = 0; i < 1 + kB; ++i) tmem_st8(to + 8 * i, r + 8 * i);
+                tmem_st_wait();
+                tc_fence_before();
+                uint32_t all = 0;
+#pragma unroll
+                for (int i = 0; i < 8 + 8 * kB; ++i) all |= r[i];
+                release_warp_to_async_proxy(all);
+                if (lane == 0) mbar_arrive(smem_addr(&scaled[slot]));
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
     } else {
         const int quarter = warp & 3;   // the TMEM lanes that this warp may read
         int n_tile = 0;
