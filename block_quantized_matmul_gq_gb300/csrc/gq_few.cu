@@ -14,7 +14,7 @@
 // every 12 cycles, 48 issue slots, so with issue slots half filled instructions and the latencies
 // between them come before memory as the limit: 304 CTAs of 8 warps (128 registers) issue in 38 %
 // (Q8_0: the shared-memory queue) to 53 % (Q4_K) of the cycles, tensor cores are at 12 to 18 %,
-// DRAM at 20 to 35 %. Measured, as a graph on a GB300: 11008 x 4096 MXFP4 times 13 tokens is
+// DRAM at 20 to 35 %. Measured, as a graph on a GB300: 32000 x 2048 MXFP4 times 13 tokens is
 // 23.0 us (5.4 us of bytes), an expert layer of 16 tokens over 64 Q8_0 experts 98 us (38), of 61
 // tokens over 64 Q4_K experts 148 us (33), of 4 tokens over 16 of 32 MXFP4 experts 39 us (9).
 // Next to it the instruction cache: forms of this kernel with all loops unrolled (70 to 150 KB of
@@ -987,7 +987,7 @@ void use_split(Params& p, const uint8_t* ws, const SplitSpace& at) {
 // one, so the split that leaves the fewest warps idle wins, less what a join costs: 3 % a doubling
 // at 8 tokens a unit, 8 % at 16. With 1, 2, 4 and 8 warps throughout, in us: 16 tokens over 64 Q8_0
 // experts 154, 99, 104, 111; 61 over 64 Q4_K experts 167, 147, 153, 170; 4 over 16 of 32 MXFP4
-// experts 64, 41, 39, 42 (all 8 tokens a unit); 11008 x 4096 MXFP4 times 13 tokens 28.7, 23.1, 24.1,
+// experts 64, 41, 39, 42 (all 8 tokens a unit); 32000 x 2048 MXFP4 times 13 tokens 28.7, 23.1, 24.1,
 // 27.3 (16 a unit).
 int pick_kshift(int64_t units, int chunks, int warps, double join) {
     int best = 0;

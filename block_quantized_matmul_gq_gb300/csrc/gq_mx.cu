@@ -12,17 +12,19 @@
 // 128 weight rows (kBN token rows) x 256 k, i.e. rows of 128 bytes in the 128-byte swizzle, then
 // the scales as 32-row x 16-byte atoms (row r's four scales at (r % 32) 16 + (r / 32) 4), so that
 // one bulk copy brings a stage's operand. X is quantized on the way. This costs the weights one
-// more read and write (15 us of 79 for 11008 x 4096 times 2048 tokens); laid out inside the
+// more read and write (15 us of 67 for 11008 x 4096 times 2048 tokens); laid out inside the
 // product it would be paid again for every token tile, and would put warps between the copies and
 // the MMA.
 //
 // mx_gemm_kernel: one persistent CTA per SM; one thread copies, one issues MMAs (four of K = 64
-// a stage, after the copies of the scales to TMEM), four warps read one accumulator out while
-// the other fills. What bounds it: a stage's 44 KB from L2 for 128 x 192 x 256 products, and the
-// fp32 results. At M = 11008, K = 4096, N = 2048 it takes 64 us for 185 GFLOP: 0.6 GB over the
-// L2's ports, 90 MB of Y; the tensor cores, at 2900 TFLOP/s then, are busy 31 % of the time. The
-// whole call is 79 us, 2350 TFLOP/s. Tiles of 128 x 192 because two accumulators of 192 columns
-// and two sets of scales fit TMEM's 512 columns (256 would leave no room to overlap).
+// a stage), four warps bring a stage's scales from shared memory to TMEM, four read one accumulator
+// out while the other fills. (With copies of the scales issued by the MMA thread, six a stage in
+// the MMAs' own pipe, the call below took 78.7 us.) What bounds it: 11008 x 4096 times 2048 tokens
+// is 67.1 us, 2750 TFLOP/s: 15 us of preparation, then 946 tiles in 7 rounds over the SMs, where
+// 6.2 would do. Timing copies with one piece left out: 58 us without the fp32 results (90 MB,
+// and the last round's with nothing beside them), 60 us with a quarter of the MMAs, no change with
+// half of the X operand's bytes. Tiles of 128 x 192 because two accumulators of 192 columns and five
+// sets of scales fit TMEM's 512 columns (256 would leave no room to overlap).
 #include <algorithm>
 #include <atomic>
 
@@ -80,7 +82,8 @@ struct PrepareParams {
 // block (lane q: elements 4q..4q+3 and 16+4q..), as in the quantizer, a unit is 8 Each rows. Rows
 // and k that pad a record are zeros with scale 2^0. What bounds it is the latency of the reads:
 // with Each = 4 four blocks a thread are on their way (one and four, whole products in us:
-// 32000 x 2048 times 17 tokens 21.7 and 20.2, 11008 x 4096 times 2048 80.7 and 77.4; but
+// 32000 x 2048 times 17 tokens 21.7 and 20.2, 11008 x 4096 times 2048 80.7 and 77.4, before the
+// scales had warps of their own; but
 // 256 x 2048 times 64, where CTAs are few, 7.4 and 8.1).
 template <int Each>
 __global__ void __launch_bounds__(256, 4) mx_prepare_kernel(const __grid_constant__ PrepareParams p) {
@@ -399,21 +402,21 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
 
 // Below, the few-token kernel. It reads the weights once for 8 or 16 tokens and prepares only X;
 // here all weights are laid out first. Both, in us for 8, 16 and 17 tokens (there, here):
-//   M x K 2048 x 2048     5.2  7.6    6.7  7.6    6.9  7.6
-//         5632 x 2048     7.4  8.8    9.4  8.8   13.3  8.8
-//        32000 x 2048    19.2 20.2   24.2 20.2   40.5 20.2
-//        11008 x 4096    18.8 17.2   23.4 17.2   34.1 17.2
-//         2048 x 5632     9.2 14.4   12.1 14.4   12.2 14.4
+//   M x K 2048 x 2048     5.2  7.4    6.7  7.4    6.9  7.4
+//         5632 x 2048     7.4  8.6    9.4  8.6   13.3  8.6
+//        32000 x 2048    19.2 19.5   24.2 19.5   40.5 19.5
+//        11008 x 4096    18.8 16.6   23.4 16.6   34.1 16.6
+//         2048 x 5632     9.2 13.6   12.1 13.6   12.2 13.6
 constexpr int64_t kMxMinTokens = 17;
 
 // Token columns of a tile: the fewest rounds of tiles over the SMs, of which a round costs a share
 // that does not depend on its columns (about 250 columns' worth), and the last one's results leave
 // with nothing beside them. In us with 64, 128 and 192 columns (tiles over 152 SMs in brackets):
-//   2048 x 2048, N = 512    9.0 (1)   9.9 (1)  11.2 (1)
-//   2048 x 2048, N = 2048  22.0 (4)  15.9 (2)  17.7 (2)
-//   5632 x 2048, N = 256   13.3 (2)  10.6 (1)  12.1 (1)
-//   5632 x 2048, N = 512   17.4 (3)  14.8 (2)  12.5 (1)
-//   11008 x 4096, N = 2048 148.9 (19) 91.0 (10) 78.6 (7)
+//   2048 x 2048, N = 512    8.5 (1)   9.4 (1)  10.3 (1)
+//   2048 x 2048, N = 2048  20.3 (4)  15.1 (2)  16.0 (2)
+//   5632 x 2048, N = 256   12.3 (2)  10.0 (1)  11.1 (1)
+//   5632 x 2048, N = 512   16.0 (3)  13.9 (2)  11.5 (1)
+//   11008 x 4096, N = 2048 131.5 (19) 81.6 (10) 66.2 (7)
 int bn_for(int64_t M, int64_t N) {
     constexpr int64_t kSms = 152;   // a GB300's; the workspace's size is asked for without a device
     const int64_t m_tiles = (M + kBM - 1) / kBM;
