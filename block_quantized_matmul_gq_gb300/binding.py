@@ -181,8 +181,10 @@ def _type(t) -> int:
 
 
 # torch's current stream of a device as an address, without building a Stream object for it
-# (2.9 us a call).
+# (2.9 us a call); the current device without a check that CUDA has been initialised (every
+# call has a CUDA or pinned tensor in hand by then).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None) -> int:
@@ -190,10 +192,12 @@ def _stream(stream=None) -> int:
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libgq has no CPU path)")
     if t.dtype != dtype:
@@ -206,6 +210,8 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
 def _act(t: torch.Tensor, dtype, name: str) -> int:
     """X, Y, gamma: a CUDA tensor, or a pinned (page-locked) host tensor, which the device
     addresses directly (include/gq.h: the kernels read and write it over the host link)."""
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
     if not (t.is_cuda or t.is_pinned()):
         raise ValueError(f"{name} must be a CUDA tensor or pinned host memory "
                          "(libgq has no CPU path)")
@@ -411,7 +417,7 @@ def mul_mat_q8x_batched(problems, t, N: int, stream=None) -> None:
 def _call_stream(stream, *tensors) -> int:
     """The stream of a call on these tensors: CUDA ones must live on the current device, where
     the library launches (get_device() is -1 for host memory)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     for t in tensors:
         at = t.get_device()
         if at != dev and at >= 0:
