@@ -123,8 +123,9 @@ cudaError_t internal_workspace(cudaStream_t s, size_t bytes, void** out) {
 }
 
 // Workspace of the MXFP4 and expert calls without one of their own: a buffer per (device,
-// stream), apart from the one above. A call holds the lock until all its kernels are queued, so
-// that calls from several threads on one stream do not interleave in the buffer. Refused while
+// stream), apart from the one above. A call holds its lock until all its kernels are queued, so
+// that calls from several threads on one stream do not interleave in the buffer; calls on other
+// streams do not wait for it. Refused while
 // the stream is being captured: a graph would keep the address of a buffer that a later, larger
 // call frees, and that calls share in stream order, which replays do not respect. The _ws forms
 // are the ones to capture.
@@ -134,8 +135,13 @@ struct CallSpace {
 };
 
 cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) {
-    static std::mutex mu;
-    static std::map<std::pair<int, void*>, std::pair<void*, size_t>> buffers;
+    struct Buffer {
+        std::mutex mu;
+        void* ptr = nullptr;
+        size_t bytes = 0;
+    };
+    static std::mutex mu;   // of the map; its entries stay where they are
+    static std::map<std::pair<int, void*>, Buffer> buffers;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(s, &cap);
     if (e != cudaSuccess) return e;
@@ -143,19 +149,27 @@ cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) {
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::unique_lock<std::mutex> lock(mu);
-    auto& entry = buffers[std::make_pair(dev, static_cast<void*>(s))];
-    if (entry.second < bytes) {
+    Buffer* buffer;
+    {
+        std::lock_guard<std::mutex> guard(mu);
+        buffer = &buffers[std::make_pair(dev, static_cast<void*>(s))];
+    }
+    std::unique_lock<std::mutex> lock(buffer->mu);
+    if (buffer->bytes < bytes) {
         e = cudaStreamSynchronize(s);   // the queued calls may still use the old buffer
         if (e != cudaSuccess) return e;
-        if (entry.first) cudaFree(entry.first);
-        entry = {nullptr, 0};
-        void* p = nullptr;
-        e = cudaMalloc(&p, bytes);
-        if (e != cudaSuccess) return e;
-        entry = {p, bytes};
+        if (buffer->ptr) cudaFree(buffer->ptr);
+        buffer->ptr = nullptr;
+        buffer->bytes = 0;
+        e = cudaMalloc(&buffer->ptr, bytes);
+        if (e != cudaSuccess) {
+            cudaGetLastError();   // reported here, not by a later launch
+            buffer->ptr = nullptr;
+            return e;
+        }
+        buffer->bytes = bytes;
     }
-    out->ptr = entry.first;
+    out->ptr = buffer->ptr;
     out->lock = std::move(lock);
     return cudaSuccess;
 }
