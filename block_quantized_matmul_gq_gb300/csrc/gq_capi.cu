@@ -125,16 +125,16 @@ cudaError_t internal_workspace(cudaStream_t s, size_t bytes, void** out) {
 // Workspace of the MXFP4 and expert calls without one of their own: a buffer per (device,
 // stream), apart from the one above. A call holds its lock until all its kernels are queued, so
 // that calls from several threads on one stream do not interleave in the buffer; calls on other
-// streams do not wait for it. Refused while
-// the stream is being captured: a graph would keep the address of a buffer that a later, larger
-// call frees, and that calls share in stream order, which replays do not respect. The _ws forms
-// are the ones to capture.
+// streams do not wait for it. Refused while the stream is being captured: a graph would keep the
+// address of a buffer that a later, larger call frees, and that calls share in stream order, which
+// replays do not respect. The _ws forms are the ones to capture. No exception leaves (an entry of
+// the map needs host memory).
 struct CallSpace {
     std::unique_lock<std::mutex> lock;
     void* ptr = nullptr;
 };
 
-cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) {
+cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) try {
     struct Buffer {
         std::mutex mu;
         void* ptr = nullptr;
@@ -172,6 +172,8 @@ cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) {
     out->ptr = buffer->ptr;
     out->lock = std::move(lock);
     return cudaSuccess;
+} catch (...) {
+    return cudaErrorMemoryAllocation;
 }
 
 // Runs one validated, non-empty problem (K > 0): tensor cores when the shape qualifies,
