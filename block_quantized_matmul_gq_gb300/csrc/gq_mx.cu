@@ -12,7 +12,7 @@
 // 128 weight rows (kBN token rows) x 256 k, i.e. rows of 128 bytes in the 128-byte swizzle, then
 // the scales as 32-row x 16-byte atoms (row r's four scales at (r % 32) 16 + (r / 32) 4), so that
 // one bulk copy brings a stage's operand. X is quantized on the way. This costs the weights one
-// more read and write (15 us of 67 for 11008 x 4096 times 2048 tokens); laid out inside the
+// more read and write (15 us of 65 for 11008 x 4096 times 2048 tokens); laid out inside the
 // product it would be paid again for every token tile, and would put warps between the copies and
 // the MMA.
 //
@@ -20,10 +20,12 @@
 // a stage), four warps bring a stage's scales from shared memory to TMEM, four read one accumulator
 // out while the other fills. (With copies of the scales issued by the MMA thread, six a stage in
 // the MMAs' own pipe, the call below took 78.7 us.) What bounds it: 11008 x 4096 times 2048 tokens
-// is 67.1 us, 2750 TFLOP/s: 15 us of preparation, then 946 tiles in 7 rounds over the SMs, where
-// 6.2 would do. Timing copies with one piece left out: 58 us without the fp32 results (90 MB,
-// and the last round's with nothing beside them), 60 us with a quarter of the MMAs, no change with
-// half of the X operand's bytes. Tiles of 128 x 192 because two accumulators of 192 columns and five
+// is 65.3 us, 2840 TFLOP/s: 15 us of preparation, then 946 tiles in 7 rounds over the SMs, where
+// 6.2 would do, a stage every 0.4 us: the chain of a stage's waits, from the copy to the scales, the
+// MMAs and back, over five stages. Timing copies with one piece left out (67.1 us whole then): 58 us
+// without the fp32 results (90 MB, and the last round's with nothing beside them), 60 us with a
+// quarter of the MMAs, 63 us without the wait for scales, no change with half of the X operand's
+// bytes. Tiles of 128 x 192 because two accumulators of 192 columns and five
 // sets of scales fit TMEM's 512 columns (256 would leave no room to overlap).
 #include <algorithm>
 #include <atomic>
@@ -303,7 +305,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
                 for (int k = 0; k < p.ktiles; ++k) {
-                    ok = mbar_wait(smem_addr(&full[slot]), phase) && mbar_wait(smem_addr(&scaled[slot]), phase);
+                    // four arrivals of warps that have waited for the stage's copies: they are
+                    // here, too (a wait for `full` as well costs 1.7 us of 67)
+                    ok = mbar_wait(smem_addr(&scaled[slot]), phase);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t a = ring + slot * C::kStage, b = a + C::kA;
