@@ -7,7 +7,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include "gq_device.cuh"
 #include "gq_internal.h"
@@ -91,90 +91,92 @@ gq_status check_problem(const void* W, gq_type t, int64_t M, int64_t K, const fl
     return GQ_OK;
 }
 
-// Library-owned workspace of the prefill path, one buffer per (device, stream), grown on
-// demand. Growing waits for the stream's queued work (which may still read the old buffer)
-// and is refused while the stream is being captured into a graph.
-cudaError_t internal_workspace(cudaStream_t s, size_t bytes, void** out) {
-    static std::mutex mu;
-    static std::map<std::pair<int, void*>, std::pair<void*, size_t>> buffers;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    auto& entry = buffers[std::make_pair(dev, static_cast<void*>(s))];
-    if (entry.second >= bytes) {
-        *out = entry.first;
-        return cudaSuccess;
-    }
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(s, &cap);
-    if (e != cudaSuccess) return e;
-    if (cap != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (entry.first) cudaFree(entry.first);
-    entry = {nullptr, 0};
-    void* p = nullptr;
-    e = cudaMalloc(&p, bytes);
-    if (e != cudaSuccess) return e;
-    entry = {p, bytes};
-    *out = p;
-    return cudaSuccess;
-}
-
-// Workspace of the MXFP4 and expert calls without one of their own: a buffer per (device,
-// stream), apart from the one above. A call holds its lock until all its kernels are queued, so
-// that calls from several threads on one stream do not interleave in the buffer; calls on other
-// streams do not wait for it. Refused while the stream is being captured: a graph would keep the
-// address of a buffer that a later, larger call frees, and that calls share in stream order, which
-// replays do not respect. The _ws forms are the ones to capture. No exception leaves (an entry of
-// the map needs host memory).
-struct CallSpace {
-    std::unique_lock<std::mutex> lock;
+// Library-owned workspaces: a buffer per device, stream and kind of call (the tensor-core paths; the
+// MXFP4 and expert calls), grown on demand.
+struct Workspace {
+    std::mutex mu;   // held by the call that queues kernels into it
     void* ptr = nullptr;
+    size_t bytes = 0;
+    unsigned long long stream_id = 0;
+    bool in_graph = false;   // a captured graph has its address: not to be freed or passed on
 };
 
-cudaError_t call_space(cudaStream_t s, size_t bytes, CallSpace* out) try {
-    struct Buffer {
-        std::mutex mu;
-        void* ptr = nullptr;
-        size_t bytes = 0;
-    };
-    static std::mutex mu;   // of the map; its entries stay where they are
-    static std::map<std::pair<int, void*>, Buffer> buffers;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(s, &cap);
-    if (e != cudaSuccess) return e;
-    if (cap != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    Buffer* buffer;
-    {
-        std::lock_guard<std::mutex> guard(mu);
-        buffer = &buffers[std::make_pair(dev, static_cast<void*>(s))];
-    }
-    std::unique_lock<std::mutex> lock(buffer->mu);
-    if (buffer->bytes < bytes) {
-        e = cudaStreamSynchronize(s);   // the queued calls may still use the old buffer
+// A handle alone does not say which stream it is. cudaStreamPerThread is one handle for a stream
+// of every thread, so the thread is part of the key. A destroyed stream's handle (and an ended
+// thread's mark) may come back for another stream while its kernels still run, so the workspace
+// keeps its stream's id, which never comes back. (The id by itself cannot be the key: it cannot be
+// asked for while the stream is captured, and workspaces of streams that are gone would pile up.)
+using WorkspaceKey = std::tuple<int, cudaStream_t, const void*, bool>;   // device, handle, thread, kind
+
+// The workspace of one call, which has it until all its kernels are queued: calls from several
+// threads on one stream do not interleave in it; calls on other streams do not wait for it.
+class CallSpace {
+public:
+    // Growing, and taking over from a stream that is gone, wait for the work that may still use the
+    // buffer, and are refused while the stream is being captured into a graph. The MXFP4 and
+    // expert calls are refused then in any case: calls share the buffer in stream order, which
+    // replays do not respect; the _ws forms are the ones to capture. No exception leaves (an entry
+    // of the table needs host memory).
+    cudaError_t acquire(bool tensor_core_paths, cudaStream_t s, size_t bytes) try {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s, &cap);
         if (e != cudaSuccess) return e;
-        if (buffer->ptr) cudaFree(buffer->ptr);
-        buffer->ptr = nullptr;
-        buffer->bytes = 0;
-        e = cudaMalloc(&buffer->ptr, bytes);
-        if (e != cudaSuccess) {
-            cudaGetLastError();   // reported here, not by a later launch
-            buffer->ptr = nullptr;
-            return e;
+        const bool capturing = cap != cudaStreamCaptureStatusNone;
+        if (capturing && !tensor_core_paths) return cudaErrorStreamCaptureUnsupported;
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        unsigned long long id = 0;
+        if (!capturing) e = cudaStreamGetId(s, &id);
+        if (e != cudaSuccess) return e;
+        static thread_local char thread_mark;
+        static std::mutex mu;
+        static std::map<WorkspaceKey, Workspace> table;   // entries stay where they are
+        Workspace* w = nullptr;
+        {
+            std::lock_guard<std::mutex> guard(mu);
+            w = &table[WorkspaceKey(dev, s, s == cudaStreamPerThread ? &thread_mark : nullptr,
+                                    tensor_core_paths)];
         }
-        buffer->bytes = bytes;
+        lock_ = std::unique_lock<std::mutex>(w->mu);
+        if (capturing) {
+            if (w->bytes < bytes) return cudaErrorStreamCaptureUnsupported;
+            w->in_graph = true;
+            ptr_ = w->ptr;
+            return cudaSuccess;
+        }
+        const bool other = w->ptr && w->stream_id != id;
+        if (other || w->bytes < bytes) {
+            e = other ? cudaDeviceSynchronize() : cudaStreamSynchronize(s);
+            if (e != cudaSuccess) return e;
+            if (w->in_graph || w->bytes < bytes) {
+                if (w->ptr && !w->in_graph) cudaFree(w->ptr);
+                w->ptr = nullptr;
+                w->bytes = 0;
+                w->in_graph = false;
+                void* p = nullptr;
+                e = cudaMalloc(&p, bytes);
+                if (e != cudaSuccess) {
+                    cudaGetLastError();   // reported here, not by a later launch
+                    return e;
+                }
+                w->ptr = p;
+                w->bytes = bytes;
+            }
+            w->stream_id = id;
+        }
+        ptr_ = w->ptr;
+        return cudaSuccess;
+    } catch (...) {
+        return cudaErrorMemoryAllocation;
     }
-    out->ptr = buffer->ptr;
-    out->lock = std::move(lock);
-    return cudaSuccess;
-} catch (...) {
-    return cudaErrorMemoryAllocation;
-}
+
+    void* ptr() const { return ptr_; }
+
+private:
+    std::unique_lock<std::mutex> lock_;
+    void* ptr_ = nullptr;
+};
 
 // Runs one validated, non-empty problem (K > 0): tensor cores when the shape qualifies,
 // else the decode kernels. `ws` may be NULL (library workspace is used then).
@@ -184,8 +186,8 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
         const size_t need = static_cast<size_t>(gq::few_workspace_bytes(p.K, N));
         CallSpace space;
         if (ws == nullptr) {
-            if (call_space(s, need, &space) != cudaSuccess) return GQ_ERR_CUDA;
-            ws = space.ptr;
+            if (space.acquire(false, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            ws = space.ptr();
             ws_bytes = need;
         } else if (ws_bytes < need || !aligned(ws, 256)) {
             return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -196,8 +198,10 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
     if (gq::gemv_tc_eligible(t, p, N)) {
         const size_t need = static_cast<size_t>(gq::gemv_tc_workspace_bytes(t, &p, 1, N));
         void* w = ws;
+        CallSpace space;
         if (w == nullptr) {
-            if (internal_workspace(s, need, &w) != cudaSuccess) return GQ_ERR_CUDA;
+            if (space.acquire(true, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            w = space.ptr();
         } else if (ws_bytes < need || !aligned(ws, 256)) {
             return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
         }
@@ -206,8 +210,10 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
     if (gq::gemm_eligible(t, p, N)) {
         const size_t need = static_cast<size_t>(gq::gemm_workspace_bytes(p.K, N));
         void* w = ws;
+        CallSpace space;
         if (w == nullptr) {
-            if (internal_workspace(s, need, &w) != cudaSuccess) return GQ_ERR_CUDA;
+            if (space.acquire(true, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            w = space.ptr();
             ws_bytes = need;
         } else if (ws_bytes < need || !aligned(ws, 256)) {
             return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -359,10 +365,9 @@ gq_status run_batch(gq_type t, int64_t N, BatchPlan* plan, void* ws, size_t ws_b
     CallSpace space;
     if (plan->ws_bytes > 0) {
         if (ws == nullptr) {
-            const cudaError_t e = t == GQ_TYPE_MXFP4 ? call_space(s, plan->ws_bytes, &space)
-                                                     : internal_workspace(s, plan->ws_bytes, &ws);
-            if (e != cudaSuccess) return GQ_ERR_CUDA;
-            if (t == GQ_TYPE_MXFP4) ws = space.ptr;
+            if (space.acquire(t != GQ_TYPE_MXFP4, s, plan->ws_bytes) != cudaSuccess)
+                return GQ_ERR_CUDA;
+            ws = space.ptr();
             ws_bytes = plan->ws_bytes;
         } else if (ws_bytes < plan->ws_bytes || !aligned(ws, 256)) {
             return ws_bytes < plan->ws_bytes ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -437,12 +442,9 @@ gq_status gq_mul_mat_rmsnorm(const void* W_blocks, gq_type t, int64_t M, int64_t
     // Otherwise: Xhat = RMSNorm(X) into library workspace, then the plain product on it.
     const size_t xb = (static_cast<size_t>(N * K) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
-    void* w = nullptr;
     CallSpace space;
-    if ((t == GQ_TYPE_MXFP4 ? call_space(s, xb + down, &space)
-                            : internal_workspace(s, xb + down, &w)) != cudaSuccess)
-        return GQ_ERR_CUDA;
-    if (t == GQ_TYPE_MXFP4) w = space.ptr;
+    if (space.acquire(t != GQ_TYPE_MXFP4, s, xb + down) != cudaSuccess) return GQ_ERR_CUDA;
+    void* w = space.ptr();
     float* xhat = static_cast<float*>(w);
     cudaError_t e = gq::launch_rmsnorm_x(X, gamma, eps, N, K, xhat, s);
     if (e != cudaSuccess) return GQ_ERR_CUDA;
@@ -466,12 +468,9 @@ gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int
     // Otherwise: G and U into library workspace by two plain products, then Swish(G) * U.
     const size_t yb = (static_cast<size_t>(N * M) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
-    void* w = nullptr;
     CallSpace space;
-    if ((t == GQ_TYPE_MXFP4 ? call_space(s, 2 * yb + down, &space)
-                            : internal_workspace(s, 2 * yb + down, &w)) != cudaSuccess)
-        return GQ_ERR_CUDA;
-    if (t == GQ_TYPE_MXFP4) w = space.ptr;
+    if (space.acquire(t != GQ_TYPE_MXFP4, s, 2 * yb + down) != cudaSuccess) return GQ_ERR_CUDA;
+    void* w = space.ptr();
     float* G = static_cast<float*>(w);
     float* U = reinterpret_cast<float*>(static_cast<uint8_t*>(w) + yb);
     void* dws = static_cast<uint8_t*>(w) + 2 * yb;
@@ -576,10 +575,10 @@ gq_status gq_mul_mat_mx4x(const void* W_blocks, gq_type t, int64_t M, int64_t K,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
     CallSpace space;
-    if (call_space(s, gq_mul_mat_mx4x_workspace_size(t, M, K, N), &space) != cudaSuccess)
+    if (space.acquire(false, s, gq_mul_mat_mx4x_workspace_size(t, M, K, N)) != cudaSuccess)
         return GQ_ERR_CUDA;
     const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
-    return from_cuda(gq::launch_mx4x(p, N, space.ptr, s));
+    return from_cuda(gq::launch_mx4x(p, N, space.ptr(), s));
 }
 
 gq_status gq_moe_route(const float* logits, int64_t N, int64_t E, int32_t top_k, int32_t renorm,
@@ -667,9 +666,9 @@ gq_status gq_moe_swiglu(const gq_moe_experts* experts, const float* X, int64_t N
     if (st != GQ_OK || !run) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallSpace space;
-    if (call_space(s, static_cast<size_t>(gq::moe_workspace_bytes(m)), &space) != cudaSuccess)
+    if (space.acquire(false, s, static_cast<size_t>(gq::moe_workspace_bytes(m))) != cudaSuccess)
         return GQ_ERR_CUDA;
-    return from_cuda(gq::launch_moe(m, space.ptr, s));
+    return from_cuda(gq::launch_moe(m, space.ptr(), s));
 }
 
 gq_status gq_get_last_error(void* stream) {

@@ -238,7 +238,11 @@ size_t gq_mul_mat_workspace_size(gq_type t, int64_t M, int64_t K, int64_t N);
  * GQ_ERR_SHAPE if it is too small, GQ_ERR_ALIGN if misaligned.
  * gq_mul_mat itself uses a library-owned workspace for the tensor-core path: one device
  * buffer per (device, stream), allocated on first need and grown when a larger shape
- * arrives (growing synchronizes that stream and is refused, GQ_ERR_CUDA, during capture).
+ * arrives (growing synchronizes that stream and is refused, GQ_ERR_CUDA, during capture; a
+ * buffer that a captured graph has the address of is not freed). cudaStreamPerThread has a
+ * buffer in every thread. The first call on a new stream that was given a destroyed one's
+ * handle waits for the device. Calls with library-owned workspaces may be made from several
+ * threads at once, on one stream or on several.
  */
 gq_status gq_mul_mat_ws(const void* W_blocks, gq_type t, int64_t M, int64_t K,
                         const float* X, int64_t N, float* Y, void* workspace,
