@@ -53,7 +53,7 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 
 bool known_type(gq_type t) { return gq::block_bytes_of(t) != 0; }
 
-gq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA; }
+using gq::from_cuda;
 
 // Shapes: non-negative, K a multiple of the type's block (32 weights; 256 for Q4_K), every
 // dimension and product in range. The type must be known.
@@ -117,7 +117,14 @@ public:
     // expert calls are refused then in any case: calls share the buffer in stream order, which
     // replays do not respect; the _ws forms are the ones to capture. No exception leaves (an entry
     // of the table needs host memory).
-    cudaError_t acquire(bool tensor_core_paths, cudaStream_t s, size_t bytes) try {
+    gq_status acquire(bool tensor_core_paths, cudaStream_t s, size_t bytes) {
+        return from_cuda(take(tensor_core_paths, s, bytes));
+    }
+
+    void* ptr() const { return ptr_; }
+
+private:
+    cudaError_t take(bool tensor_core_paths, cudaStream_t s, size_t bytes) try {
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
         cudaError_t e = cudaStreamIsCapturing(s, &cap);
         if (e != cudaSuccess) return e;
@@ -156,10 +163,7 @@ public:
                 w->in_graph = false;
                 void* p = nullptr;
                 e = cudaMalloc(&p, bytes);
-                if (e != cudaSuccess) {
-                    cudaGetLastError();   // reported here, not by a later launch
-                    return e;
-                }
+                if (e != cudaSuccess) return e;
                 w->ptr = p;
                 w->bytes = bytes;
             }
@@ -171,9 +175,6 @@ public:
         return cudaErrorMemoryAllocation;
     }
 
-    void* ptr() const { return ptr_; }
-
-private:
     std::unique_lock<std::mutex> lock_;
     void* ptr_ = nullptr;
 };
@@ -186,7 +187,7 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
         const size_t need = static_cast<size_t>(gq::few_workspace_bytes(p.K, N));
         CallSpace space;
         if (ws == nullptr) {
-            if (space.acquire(false, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            if (space.acquire(false, s, need) != GQ_OK) return GQ_ERR_CUDA;
             ws = space.ptr();
             ws_bytes = need;
         } else if (ws_bytes < need || !aligned(ws, 256)) {
@@ -200,7 +201,7 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
         void* w = ws;
         CallSpace space;
         if (w == nullptr) {
-            if (space.acquire(true, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            if (space.acquire(true, s, need) != GQ_OK) return GQ_ERR_CUDA;
             w = space.ptr();
         } else if (ws_bytes < need || !aligned(ws, 256)) {
             return ws_bytes < need ? GQ_ERR_SHAPE : GQ_ERR_ALIGN;
@@ -212,7 +213,7 @@ gq_status run_one(gq_type t, const gq::MatProblem& p, int64_t N, void* ws, size_
         void* w = ws;
         CallSpace space;
         if (w == nullptr) {
-            if (space.acquire(true, s, need) != cudaSuccess) return GQ_ERR_CUDA;
+            if (space.acquire(true, s, need) != GQ_OK) return GQ_ERR_CUDA;
             w = space.ptr();
             ws_bytes = need;
         } else if (ws_bytes < need || !aligned(ws, 256)) {
@@ -335,7 +336,7 @@ gq_status plan_batch(const gq_mul_mat_problem* problems, int32_t count, gq_type 
         const gq_mul_mat_problem& p = problems[i];
         if (p.M == 0 || N == 0) continue;
         if (p.K == 0) {
-            if (zero_k0 && cudaMemsetAsync(p.Y, 0, sizeof(float) * N * p.M, s) != cudaSuccess)
+            if (zero_k0 && from_cuda(cudaMemsetAsync(p.Y, 0, sizeof(float) * N * p.M, s)) != GQ_OK)
                 return GQ_ERR_CUDA;
             continue;
         }
@@ -365,7 +366,7 @@ gq_status run_batch(gq_type t, int64_t N, BatchPlan* plan, void* ws, size_t ws_b
     CallSpace space;
     if (plan->ws_bytes > 0) {
         if (ws == nullptr) {
-            if (space.acquire(t != GQ_TYPE_MXFP4, s, plan->ws_bytes) != cudaSuccess)
+            if (space.acquire(t != GQ_TYPE_MXFP4, s, plan->ws_bytes) != GQ_OK)
                 return GQ_ERR_CUDA;
             ws = space.ptr();
             ws_bytes = plan->ws_bytes;
@@ -407,7 +408,7 @@ gq_status check_q8x(const void* W, gq_type t, int64_t M, int64_t K, const float*
     gq_status st = check_problem(W, t, M, K, X, N, Y, &empty);
     if (st != GQ_OK || empty) return st;
     if (K == 0) {
-        if (zero_k0 && cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s) != cudaSuccess)
+        if (zero_k0 && from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s)) != GQ_OK)
             return GQ_ERR_CUDA;
         return GQ_OK;
     }
@@ -443,11 +444,11 @@ gq_status gq_mul_mat_rmsnorm(const void* W_blocks, gq_type t, int64_t M, int64_t
     const size_t xb = (static_cast<size_t>(N * K) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     CallSpace space;
-    if (space.acquire(t != GQ_TYPE_MXFP4, s, xb + down) != cudaSuccess) return GQ_ERR_CUDA;
+    if (space.acquire(t != GQ_TYPE_MXFP4, s, xb + down) != GQ_OK) return GQ_ERR_CUDA;
     void* w = space.ptr();
     float* xhat = static_cast<float*>(w);
     cudaError_t e = gq::launch_rmsnorm_x(X, gamma, eps, N, K, xhat, s);
-    if (e != cudaSuccess) return GQ_ERR_CUDA;
+    if (e != cudaSuccess) return from_cuda(e);
     const gq::MatProblem q{static_cast<const uint8_t*>(W_blocks), xhat, Y, M, K};
     return run_one(t, q, N, static_cast<uint8_t*>(w) + xb, down, s);
 }
@@ -469,7 +470,7 @@ gq_status gq_mul_mat_swiglu(const void* W_gate, const void* W_up, gq_type t, int
     const size_t yb = (static_cast<size_t>(N * M) * 4 + 255) / 256 * 256;
     const size_t down = gq_mul_mat_workspace_size(t, M, K, N);
     CallSpace space;
-    if (space.acquire(t != GQ_TYPE_MXFP4, s, 2 * yb + down) != cudaSuccess) return GQ_ERR_CUDA;
+    if (space.acquire(t != GQ_TYPE_MXFP4, s, 2 * yb + down) != GQ_OK) return GQ_ERR_CUDA;
     void* w = space.ptr();
     float* G = static_cast<float*>(w);
     float* U = reinterpret_cast<float*>(static_cast<uint8_t*>(w) + yb);
@@ -575,7 +576,7 @@ gq_status gq_mul_mat_mx4x(const void* W_blocks, gq_type t, int64_t M, int64_t K,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
     CallSpace space;
-    if (space.acquire(false, s, gq_mul_mat_mx4x_workspace_size(t, M, K, N)) != cudaSuccess)
+    if (space.acquire(false, s, gq_mul_mat_mx4x_workspace_size(t, M, K, N)) != GQ_OK)
         return GQ_ERR_CUDA;
     const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
     return from_cuda(gq::launch_mx4x(p, N, space.ptr(), s));
@@ -666,22 +667,22 @@ gq_status gq_moe_swiglu(const gq_moe_experts* experts, const float* X, int64_t N
     if (st != GQ_OK || !run) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallSpace space;
-    if (space.acquire(false, s, static_cast<size_t>(gq::moe_workspace_bytes(m))) != cudaSuccess)
+    if (space.acquire(false, s, static_cast<size_t>(gq::moe_workspace_bytes(m))) != GQ_OK)
         return GQ_ERR_CUDA;
     return from_cuda(gq::launch_moe(m, space.ptr(), s));
 }
 
 gq_status gq_get_last_error(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(s) != cudaSuccess) return GQ_ERR_CUDA;
+    if (from_cuda(cudaStreamSynchronize(s)) != GQ_OK) return GQ_ERR_CUDA;
     gq::DeviceInfo* info = nullptr;
-    if (gq::current_device_info(&info) != cudaSuccess) return GQ_ERR_CUDA;
+    if (from_cuda(gq::current_device_info(&info)) != GQ_OK) return GQ_ERR_CUDA;
     unsigned word = 0;
-    if (cudaMemcpy(&word, info->status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (from_cuda(cudaMemcpy(&word, info->status, sizeof word, cudaMemcpyDeviceToHost)) != GQ_OK)
         return GQ_ERR_CUDA;
     if (word != 0) {
         const unsigned zero = 0;
-        if (cudaMemcpy(info->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
+        if (from_cuda(cudaMemcpy(info->status, &zero, sizeof zero, cudaMemcpyHostToDevice)) != GQ_OK)
             return GQ_ERR_CUDA;
         return GQ_ERR_TIMEOUT;
     }
@@ -728,7 +729,7 @@ __global__ void wait_timeout_selftest_kernel(unsigned long long limit_ns, unsign
 extern "C" gq_status gq_selftest_wait_timeout(int64_t limit_us, void* stream) {
     if (limit_us < 1 || limit_us > 10000000) return GQ_ERR_SHAPE;
     gq::DeviceInfo* info = nullptr;
-    if (gq::current_device_info(&info) != cudaSuccess) return GQ_ERR_CUDA;
+    if (from_cuda(gq::current_device_info(&info)) != GQ_OK) return GQ_ERR_CUDA;
     gq::wait_timeout_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<unsigned long long>(limit_us) * 1000ull, info->status);
     return from_cuda(cudaGetLastError());

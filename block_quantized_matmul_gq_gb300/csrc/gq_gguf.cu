@@ -357,7 +357,7 @@ gq_status gq_gguf_upload(const gq_gguf* f, int64_t i, void* dst, size_t dst_byte
     const cudaError_t e = cudaMemcpyAsync(dst, f->map + t.offset, t.nbytes,
                                           cudaMemcpyHostToDevice,
                                           static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return gq::from_cuda(e);
 }
 
 int64_t gq_gguf_find_key(const gq_gguf* f, const char* key) {

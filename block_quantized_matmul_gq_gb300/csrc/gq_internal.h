@@ -25,6 +25,14 @@ inline int block_bytes_of(gq_type t) {
     return 0;
 }
 
+// The status of a CUDA call. A refused call is reported here and does not stay behind as the last
+// error, where a later launch would find it and fail in its place.
+inline gq_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return GQ_OK;
+    (void)cudaGetLastError();
+    return GQ_ERR_CUDA;
+}
+
 // Weights per block: 32, or 256 for a Q4_K super-block; 0 for an unknown type.
 inline int block_weights_of(gq_type t) {
     return t == GQ_TYPE_Q4_K ? kQ4KWeights : (block_bytes_of(t) ? 32 : 0);

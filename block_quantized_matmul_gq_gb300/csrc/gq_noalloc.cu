@@ -73,15 +73,14 @@ extern "C" gq_status gq_mul_mat_noalloc(const void* W_blocks, gq_type t, int64_t
     if (K > 0 && (!gq::aligned_to(W_blocks, 16) || !gq::aligned_to(X, 4))) return GQ_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0)
-        return cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s) == cudaSuccess ? GQ_OK
-                                                                            : GQ_ERR_CUDA;
+        return gq::from_cuda(cudaMemsetAsync(Y, 0, sizeof(float) * N * M, s));
     const gq::MatProblem p{static_cast<const uint8_t*>(W_blocks), X, Y, M, K};
     const int64_t cap = static_cast<int64_t>(gq::kNoAllocScratchBytes);
     if (t == GQ_TYPE_MXFP4) {   // as many tokens a pass as the array holds split
         if (gq::few_tokens_that_fit(M, K, N, cap) < 1) return GQ_ERR_SHAPE;
         void* scratch = nullptr;
-        if (gq::noalloc_scratch(&scratch) != cudaSuccess) return GQ_ERR_CUDA;
-        return gq::launch_few_mul_mat(p, N, scratch, cap, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+        if (gq::from_cuda(gq::noalloc_scratch(&scratch)) != GQ_OK) return GQ_ERR_CUDA;
+        return gq::from_cuda(gq::launch_few_mul_mat(p, N, scratch, cap, s));
     }
     // Tensor-core decode (3..64 tokens): its bf16 X tiles, partial sums and split-tile
     // counters fit the array for any K up to ~390k; x_tiles_kernel rewrites the tiles and
@@ -89,15 +88,15 @@ extern "C" gq_status gq_mul_mat_noalloc(const void* W_blocks, gq_type t, int64_t
     // kernels, which need no workspace.
     if (gq::gemv_tc_eligible(t, p, N)) {
         if (gq::gemv_tc_workspace_bytes(t, &p, 1, N) > cap)
-            return gq::launch_mul_mat(t, &p, 1, N, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+            return gq::from_cuda(gq::launch_mul_mat(t, &p, 1, N, s));
         void* scratch = nullptr;
-        if (gq::noalloc_scratch(&scratch) != cudaSuccess) return GQ_ERR_CUDA;
-        return gq::launch_gemv_tc(t, &p, 1, N, scratch, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+        if (gq::from_cuda(gq::noalloc_scratch(&scratch)) != GQ_OK) return GQ_ERR_CUDA;
+        return gq::from_cuda(gq::launch_gemv_tc(t, &p, 1, N, scratch, s));
     }
     if (!gq::gemm_eligible(t, p, N))   // CUDA-core decode: needs no workspace at all
-        return gq::launch_mul_mat(t, &p, 1, N, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+        return gq::from_cuda(gq::launch_mul_mat(t, &p, 1, N, s));
     if (gq::gemm_x_bytes(K, N) > cap) return GQ_ERR_SHAPE;   // N * K beyond the fixed array
     void* scratch = nullptr;
-    if (gq::noalloc_scratch(&scratch) != cudaSuccess) return GQ_ERR_CUDA;
-    return gq::launch_gemm(t, p, N, scratch, cap, s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    if (gq::from_cuda(gq::noalloc_scratch(&scratch)) != GQ_OK) return GQ_ERR_CUDA;
+    return gq::from_cuda(gq::launch_gemm(t, p, N, scratch, cap, s));
 }
