@@ -222,10 +222,24 @@ def _act(t: torch.Tensor, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _out_like(X: torch.Tensor, shape) -> torch.Tensor:
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream` (None: torch's current one), in memory of that stream: from
+    the current one's, it could be a block that kernels queued there still use. It is not handed on
+    either before the current stream has done with it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream())
+    return out
+
+
+def _out_like(X: torch.Tensor, shape, stream) -> torch.Tensor:
     """Y where X lives: on X's device, or pinned host memory for a pinned host X."""
     if X.is_cuda:
-        return torch.empty(shape, dtype=torch.float32, device=X.device)
+        return _new(shape, torch.float32, X.device, stream)
     return torch.empty(shape, dtype=torch.float32, pin_memory=True)
 
 
@@ -241,7 +255,7 @@ def quantize(W: torch.Tensor, t, out: torch.Tensor | None = None, stream=None) -
     """fp32 (M, K) CUDA tensor -> uint8 (M, row_bytes) blocks."""
     M, K = W.shape
     if out is None:
-        out = torch.empty((M, row_bytes(t, K)), dtype=torch.uint8, device=W.device)
+        out = _new((M, row_bytes(t, K)), torch.uint8, W.device, stream)
     fn = getattr(lib, _QUANTIZE[_type(t)])
     _check(fn(_dev(W, torch.float32, "W"), M, K, _dev(out, torch.uint8, "W_blocks"),
               _stream(stream)), "gq_quantize")
@@ -251,7 +265,7 @@ def quantize(W: torch.Tensor, t, out: torch.Tensor | None = None, stream=None) -
 def dequantize(blocks: torch.Tensor, t, M: int, K: int, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float32, device=blocks.device)
+        out = _new((M, K), torch.float32, blocks.device, stream)
     _check(lib.gq_dequantize(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
                              _dev(out, torch.float32, "W_out"), _stream(stream)),
            "gq_dequantize")
@@ -267,7 +281,7 @@ def mul_mat(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     if X.shape[1] != K:
         raise ValueError("X must be (N, K)")
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _check(lib.gq_mul_mat(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
                           _act(X, torch.float32, "X"), N, _act(out, torch.float32, "Y"),
                           _stream(stream)), "gq_mul_mat")
@@ -286,7 +300,7 @@ def mul_mat_ws(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
         X = X.view(1, -1)
     N = X.shape[0]
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     wp = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     wn = workspace.numel() if workspace is not None else 0
     _check(lib.gq_mul_mat_ws(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
@@ -303,7 +317,7 @@ def mul_mat_noalloc(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
         X = X.view(1, -1)
     N = X.shape[0]
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _check(lib.gq_mul_mat_noalloc(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
                                   _act(X, torch.float32, "X"), N,
                                   _act(out, torch.float32, "Y"), _stream(stream)),
@@ -365,7 +379,7 @@ def mul_mat_q8x(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     if X.shape[1] != K:
         raise ValueError("X must be (N, K)")
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _check(lib.gq_mul_mat_q8x(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
                               _act(X, torch.float32, "X"), N, _act(out, torch.float32, "Y"),
                               _stream(stream)), "gq_mul_mat_q8x")
@@ -382,7 +396,7 @@ def mul_mat_rmsnorm(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     if X.shape[1] != K or gamma.numel() != K:
         raise ValueError("X must be (N, K) and gamma (K,)")
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _check(lib.gq_mul_mat_rmsnorm(_dev(blocks, torch.uint8, "W_blocks"), _type(t), M, K,
                                   _act(X, torch.float32, "X"), _act(gamma, torch.float32, "gamma"),
                                   float(eps), N, _act(out, torch.float32, "Y"), _stream(stream)),
@@ -399,7 +413,7 @@ def mul_mat_swiglu(gate: torch.Tensor, up: torch.Tensor, t, M: int, K: int, X: t
     if X.shape[1] != K:
         raise ValueError("X must be (N, K)")
     if out is None:
-        out = _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _check(lib.gq_mul_mat_swiglu(_dev(gate, torch.uint8, "W_gate"), _dev(up, torch.uint8, "W_up"),
                                  _type(t), M, K, _act(X, torch.float32, "X"), N,
                                  _act(out, torch.float32, "H"), _stream(stream)),
@@ -425,15 +439,6 @@ def _call_stream(stream, *tensors) -> int:
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return _stream(stream)
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output of a call on `stream` (None: torch's current one)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    out = torch.empty(shape, dtype=dtype, device=device)
-    out.record_stream(stream)   # else its memory could be handed on before the call has written it
-    return out
 
 
 _BLOCKS = {Q4_0: (32, 18), Q8_0: (32, 34), Q4_K: (256, 144), MXFP4: (32, 17)}
@@ -467,7 +472,7 @@ def mul_mat_mx4x(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     t = _type(t)
     _has(blocks, _matrix_bytes(t, M, K), "W_blocks")
     if out is None:
-        out = _new((N, M), torch.float32, X.device, stream) if X.is_cuda else _out_like(X, (N, M))
+        out = _out_like(X, (N, M), stream)
     _has(out, N * M, "Y")
     args = (_dev(blocks, torch.uint8, "W_blocks"), t, M, K, _act(X, torch.float32, "X"), N,
             _act(out, torch.float32, "Y"))

@@ -109,9 +109,10 @@ class GGUFFile:
         info = self.tensor(i)
         try:
             btype, M, K = self.matrix(i)
-            out = torch.empty((M, binding.row_bytes(btype, K)), dtype=torch.uint8, device=device)
+            shape = (M, binding.row_bytes(btype, K))
         except binding.GQError:
-            out = torch.empty((info.nbytes,), dtype=torch.uint8, device=device)
+            shape = (info.nbytes,)
+        out = binding._new(shape, torch.uint8, torch.device(device), stream)
         binding._check(binding.lib.gq_gguf_upload(self._h, i, out.data_ptr(), out.numel(),
                                                   binding._stream(stream)),
                        "gq_gguf_upload")
