@@ -476,10 +476,11 @@ def mul_mat_mx4x(blocks: torch.Tensor, t, M: int, K: int, X: torch.Tensor,
     _has(out, N * M, "Y")
     args = (_dev(blocks, torch.uint8, "W_blocks"), t, M, K, _act(X, torch.float32, "X"), N,
             _act(out, torch.float32, "Y"))
-    s = _call_stream(stream, blocks, X, out)
     if workspace is None:
+        s = _call_stream(stream, blocks, X, out)
         _check(lib.gq_mul_mat_mx4x(*args, s), "gq_mul_mat_mx4x")
     else:
+        s = _call_stream(stream, blocks, X, out, workspace)
         _check(lib.gq_mul_mat_mx4x_ws(*args, _dev(workspace, torch.uint8, "workspace"),
                                       workspace.numel(), s), "gq_mul_mat_mx4x_ws")
     return out
@@ -508,7 +509,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, stream=None
 
 class MoeExperts:
     """The experts of one layer: gate and up (E * F rows of D weights) and down (E * D rows of F)
-    as uint8 CUDA tensors of blocks, types `t` and `t_down` (default: the same)."""
+    as uint8 tensors of blocks on one CUDA device, types `t` and `t_down` (default: the same)."""
 
     def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, t, E: int, D: int,
                  F: int, t_down=None):
@@ -522,6 +523,8 @@ class MoeExperts:
         self.tensors = (gate, up, down)   # kept alive: the struct holds raw pointers
         self.c = Experts(_dev(gate, torch.uint8, "W_gate"), _dev(up, torch.uint8, "W_up"),
                          _dev(down, torch.uint8, "W_down"), t, t_down, E, D, F)
+        if not gate.get_device() == up.get_device() == down.get_device():
+            raise ValueError("W_gate, W_up and W_down must be on one device")
 
     def workspace_size(self, N: int, top_k: int) -> int:
         return int(lib.gq_moe_workspace_size(ctypes.byref(self.c), N, top_k))
@@ -542,10 +545,11 @@ def moe_swiglu(experts: MoeExperts, X: torch.Tensor, ids: torch.Tensor, weights:
     _has(out, N * experts.D, "Y")
     args = (ctypes.byref(experts.c), _dev(X, torch.float32, "X"), N, _dev(ids, torch.int32, "ids"),
             _dev(weights, torch.float32, "weights"), ids.shape[1], _dev(out, torch.float32, "Y"))
-    s = _call_stream(stream, X, ids, weights, out, experts.tensors[0])
     if workspace is None:
+        s = _call_stream(stream, X, ids, weights, out, experts.tensors[0])
         _check(lib.gq_moe_swiglu(*args, s), "gq_moe_swiglu")
     else:
+        s = _call_stream(stream, X, ids, weights, out, experts.tensors[0], workspace)
         _check(lib.gq_moe_swiglu_ws(*args, _dev(workspace, torch.uint8, "workspace"),
                                     workspace.numel(), s), "gq_moe_swiglu_ws")
     return out
