@@ -94,7 +94,7 @@ class GGUFFile:
                                      shape=(info.nbytes,)).copy()
 
     def matrix(self, name_or_index):
-        """(block type name, M, K) of a 2-D Q4_0 / Q8_0 / Q4_K tensor."""
+        """(block type name, M, K) of a 2-D Q4_0 / Q8_0 / Q4_K / MXFP4 tensor."""
         i = self._index(name_or_index)
         t, M, K = ctypes.c_int(), ctypes.c_int64(), ctypes.c_int64()
         binding._check(binding.lib.gq_gguf_tensor_matrix(self._h, i, ctypes.byref(t),
@@ -104,7 +104,8 @@ class GGUFFile:
 
     def upload(self, name_or_index, device, stream=None) -> torch.Tensor:
         """Copies the tensor to `device`: an (M, row_bytes) uint8 tensor for a block-type
-        matrix (W_blocks of binding.mul_mat), else a flat uint8 tensor of its bytes."""
+        matrix (W_blocks of binding.mul_mat), else a flat uint8 tensor of its bytes (the
+        experts of a layer, a 3-D tensor of shape (K, rows, E): as binding.MoeExperts takes them)."""
         i = self._index(name_or_index)
         info = self.tensor(i)
         try:

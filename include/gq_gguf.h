@@ -23,7 +23,10 @@
  * The ggml type ids of the block formats equal gq_type: 2 Q4_0, 8 Q8_0, 12 Q4_K, 39 MXFP4, and
  * a 2-D weight tensor of those types is stored exactly as gq_mul_mat reads W_blocks:
  * M = ne[1] rows of gq_row_bytes(type, K = ne[0]) bytes each. So a tensor goes from the
- * file to the GPU with one copy and no conversion.
+ * file to the GPU with one copy and no conversion. The experts of a layer, one 3-D tensor with
+ * ne = (K, rows, E), are stored exactly as a gq_moe_experts array: gq_gguf_upload copies them,
+ * and E * ne[1] rows of ne[0] weights are their matrix (gq_gguf_tensor_matrix, which is about
+ * gq_mul_mat's arguments, refuses them).
  *
  * Every function here runs on the host. A gq_gguf handle owns the mapping and every string
  * it hands out; they stay valid until gq_gguf_close. Handles are read-only after
