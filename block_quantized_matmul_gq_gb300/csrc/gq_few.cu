@@ -23,6 +23,9 @@
 // pass through shared memory once more, fp16 scales would have to be applied outside, and its
 // 128-row tiles leave most SMs without work here. (The microscaled product, whose scales the
 // tensor cores apply, does use it: gq_mx.cu.)
+// More tokens than one group: every group unpacks the weights again (from L2), so prompts cost in
+// proportion, far from their bytes: 32000 x 2048 MXFP4 times 512 tokens 479 us (35 of operations and
+// bytes), 512 tokens over 64 Q4_K experts, 8 each, in 8 passes 1220 us.
 //
 // Layout of the work. A unit is (a group of up to 8 NT tokens, 32 result rows); a row warp has a
 // run of consecutive units, so that those of one group follow each other and share activations
@@ -1153,7 +1156,10 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const int pairs = static_cast<int>(n * m.top_k);
         // One tile of 8 tokens, or two where an expert at work has more on average than fit one
         // in most cases (61 tokens over 64 Q4_K experts, 7.6 pairs an expert: 147 us with one,
-        // 167 us with two); `groups` as if the pairs were spread by chance.
+        // 167 us with two; the border of ten is between that point and 16, not measured). The two-tile
+        // kernels do not fit their 128 registers: bytes spilled for Q4_K 140 (gate and up) and 356
+        // (down), 8 to 64 for the other types (one tile: at most 16), so part of the 167 us may be
+        // theirs. `groups` as if the pairs were spread by chance.
         const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
         const double mean = pairs / active;
         const bool wide = mean > 10.0;

@@ -4,9 +4,10 @@
 // One warp per token keeps the token's logits in registers (expert lane + 32 i) as integers in
 // the order of the floats, so a round of the selection is one maximum over the lane's values,
 // one warp maximum and one warp minimum over the lanes that hold it (the lowest index of equal
-// logits). It reads 4 E bytes a token and is bound by those rounds, a chain of two warp reductions
-// for each of the top_k, hidden by the other warps of the SM when there are many tokens: one token
-// over 64 experts takes 1.8 us (a launch), 8191 over 128 with top_k = 8 7.5 us (0.7 us of bytes).
+// logits). It reads 4 E bytes a token and is bound by those rounds, two warp reductions and the search
+// for the holder for each of the top_k: a chain for one token, instructions for many (issue slots
+// are 71 % busy). One token over 64 experts takes 1.8 us (a launch), 8191 over 128 with top_k = 8
+// 7.5 us (0.7 us of bytes).
 #include <algorithm>
 
 #include "gq_few.cuh"

@@ -411,6 +411,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx_gemm_kernel(const __grid_con
 //        32000 x 2048    19.2 19.5   24.2 19.5   40.5 19.5
 //        11008 x 4096    18.8 16.6   23.4 16.6   34.1 16.6
 //         2048 x 5632     9.2 13.6   12.1 13.6   12.2 13.6
+// The border is a number of tokens, whatever the matrix: the few-token kernel's second group begins
+// there, which doubles its time on matrices that fill the SMs. It is not each matrix's best: with 8
+// to 16 tokens the larger three lose up to 40 % to this side, with 17 the two of 2048 rows up to 11 %
+// to the other.
 constexpr int64_t kMxMinTokens = 17;
 
 // Token columns of a tile: the fewest rounds of tiles over the SMs, of which a round costs a share
