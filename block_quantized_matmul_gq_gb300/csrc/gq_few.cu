@@ -1155,11 +1155,17 @@ cudaError_t launch_moe(const MoeProblem& m, void* workspace, cudaStream_t s) {
         const MoeSpace at = moe_space(m, n);
         const int pairs = static_cast<int>(n * m.top_k);
         // One tile of 8 tokens, or two where an expert at work has more on average than fit one
-        // in most cases (61 tokens over 64 Q4_K experts, 7.6 pairs an expert: 147 us with one,
-        // 167 us with two; the border of ten is between that point and 16, not measured). The two-tile
-        // kernels do not fit their 128 registers: bytes spilled for Q4_K 140 (gate and up) and 356
-        // (down), 8 to 64 for the other types (one tile: at most 16), so part of the 167 us may be
-        // theirs. `groups` as if the pairs were spread by chance.
+        // in most cases. In us with one and two, by tokens an expert on average (4 chosen, D = 2048,
+        // F = 1024; the draw of experts moves single figures by a fifth):
+        //                       6            8           10           12           16
+        //   32 Q4_0          69.1  84.0   98.8  85.3  101.1  86.6  130.5  89.3  167.5 133.8
+        //   32 Q8_0          80.4  98.3  115.6 100.0  119.8 102.3  169.3 104.0  211.1 160.5
+        //   32 Q4_K          65.6  90.4   94.3  92.6   97.2  94.1  126.9  96.5  159.0 157.8
+        //    8 Q4_K          25.8  34.7   34.6  35.2   49.8  36.2   49.7  36.4   51.6  76.9
+        //   32 MXFP4         61.5  77.4   89.3  78.3   91.5  80.7  121.9  82.9  139.6 124.3
+        // and 61 tokens over 64 Q4_K experts, 7.6 an expert, 147 and 167. The two-tile kernels do not
+        // fit their 128 registers: bytes spilled for Q4_K 140 (gate and up) and 356 (down), 8 to 64 for
+        // the other types (one tile: at most 16). `groups` as if the pairs were spread by chance.
         const double active = m.E * (1.0 - std::pow(1.0 - 1.0 / m.E, pairs));
         const double mean = pairs / active;
         const bool wide = mean > 10.0;
