@@ -104,8 +104,9 @@ struct Workspace {
 // A handle alone does not say which stream it is. cudaStreamPerThread is one handle for a stream
 // of every thread, so the thread is part of the key. A destroyed stream's handle (and an ended
 // thread's mark) may come back for another stream while its kernels still run, so the workspace
-// keeps its stream's id, which never comes back. (The id by itself cannot be the key: it cannot be
-// asked for while the stream is captured, and workspaces of streams that are gone would pile up.)
+// keeps its stream's id, which never comes back. (The id by itself cannot be the key: asking for it
+// ends the stream's capture, if there is one, and workspaces of streams that are gone would pile
+// up. So a capture takes the buffer by the handle, as the last call on the stream left it.)
 using WorkspaceKey = std::tuple<int, cudaStream_t, const void*, bool>;   // device, handle, thread, kind
 
 // The workspace of one call, which has it until all its kernels are queued: calls from several

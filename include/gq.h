@@ -179,8 +179,9 @@ gq_status gq_quantize_q4_k(const float* W, int64_t M, int64_t K, void* W_blocks,
  * into a graph (GQ_ERR_CUDA), the _ws forms and gq_mul_mat_noalloc do not. They run on a
  * kernel for a few tokens, which reads the weights once for every 16: a prompt costs in proportion
  * (gq_mul_mat_mx4x is the fast form there, with X rounded). gq_mul_mat_batched
- * runs MXFP4 problems one after another, two launches each. gq_mul_mat_rmsnorm and gq_mul_mat_swiglu take it in
- * their composite forms; gq_mul_mat_q8x does not (GQ_ERR_TYPE; gq_mul_mat_mx4x is its kind).
+ * runs MXFP4 problems one after another, two launches each. gq_mul_mat_rmsnorm and
+ * gq_mul_mat_swiglu take it in their composite forms; gq_mul_mat_q8x does not (GQ_ERR_TYPE;
+ * gq_mul_mat_mx4x is its kind).
  * Range: X[n] is brought to a maximum in [2^14, 2^15) first, and sum_k What[m][k] X[n][k] in
  * those units must stay inside fp32's range (it does for |What| below 2^80). max|X[n]| counts
  * as at least 2^-110 in the bound. Non-finite values of a token reach that token's results

@@ -139,3 +139,42 @@ def test_a_captured_workspace_stays(gq_lib, cuda_dev):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(got_big, want_big) and (scratch == 255).all()
+
+
+def test_calls_while_another_thread_captures(gq_lib, cuda_dev):
+    """Eager calls of one thread leave the capture of another alone, and the other way round."""
+    todo, want = calls(gq_lib, cuda_dev, 0)
+    eager, captured = [[torch.zeros_like(w) for w in want] for _ in range(2)]
+    stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = torch.empty(gq_lib.workspace_size("mxfp4", 64, 64, 2), dtype=torch.uint8, device=cuda_dev)
+    q, x = gq_lib.quantize(torch.ones((64, 64), device=cuda_dev), "mxfp4"), torch.ones((2, 64), device=cuda_dev)
+    y, wrong = torch.zeros((2, 64), device=cuda_dev), []
+    tensor_cores = [2, 3, 4, 8]   # the calls that may be captured with the library's workspace
+    for s in (stream, side):
+        for f, o in zip(todo, eager):
+            f(s, o)
+    torch.cuda.synchronize()
+    for o in eager:
+        o.zero_()
+    torch.cuda.synchronize()
+
+    def run():
+        try:
+            for f, o in zip(todo, eager):
+                f(stream, o)
+        except Exception as e:
+            wrong.append(e)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        gq_lib.mul_mat_ws(q, "mxfp4", 64, 64, x, ws, out=y)
+        thread = threading.Thread(target=run)
+        thread.start()
+        thread.join()
+        for i in tensor_cores:
+            todo[i](None, captured[i])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not wrong and (y == 64).all()
+    assert all(torch.equal(a, b) for a, b in zip(eager, want))
+    assert all(torch.equal(captured[i], want[i]) for i in tensor_cores)
