@@ -209,3 +209,16 @@ def test_mean_error_of_the_expert_layer(gq_lib, cuda_dev, t, E, N, k):
     x = np.random.default_rng(N).standard_normal(x.shape).astype(np.float32)
     want, _ = ref.moe(*layer.ref, x.astype(np.float64), ids, w)
     assert off(layer.run(x, ids, w), want) <= LIMIT
+
+
+@pytest.mark.parametrize("M,K", [(2048, 2048), (5632, 544), (300, 4096)])
+@pytest.mark.parametrize("N", [12, 15, 16, 17, 18, 24])
+def test_both_sides_of_the_token_border(gq_lib, cuda_dev, M, K, N):
+    """Up to 16 tokens the workspace holds split activations alone, from 17 the weights' records, too."""
+    laid_out = gq_lib.mx4x_workspace_size("mxfp4", M, K, N) >= M * K // 2
+    assert laid_out == (N >= 17)
+    blocks = weights(M, K, 5)
+    x = np.random.default_rng(N).standard_normal((N, K), np.float32)
+    y = gq_lib.mul_mat_mx4x(torch.from_numpy(blocks).to(cuda_dev), "mxfp4", M, K, torch.from_numpy(x).to(cuda_dev))
+    want, tol = ref.product(*ref.weights("mxfp4", blocks, M, K), ref.mx_values(*ref.mx_quantize(x)))
+    assert (np.abs(y.cpu().numpy() - want) <= tol).all()
