@@ -153,17 +153,20 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
 constexpr uint32_t kMagic = 0x64006400u;       // 1024
 constexpr uint32_t kSixteenth = 0x2C002C00u;   // 1/16
 
-// The eight 4-bit codes of a word minus Z (0 or 8), as fp16 pairs (bits 0 and 16), (4 and 20),
+// The eight 4-bit codes of a word minus Z (0 or 8), times 2^-S, as fp16 pairs (bits 0 and 16), (4 and 20),
 // (8 and 24), (12 and 28).
-template <int Z>
+template <int Z, int S = 0>
 __device__ __forceinline__ void nibbles_to_f16(uint32_t w, uint32_t (&h)[4]) {
-    constexpr uint32_t kLow = Z == 8 ? 0x64086408u : 0x64006400u;     // 1024 + Z
-    constexpr uint32_t kHigh = Z == 8 ? 0xD480D480u : 0xD400D400u;    // -(64 + Z)
+    constexpr uint32_t kBoth = 0x00010001u;
+    constexpr uint32_t kOne = kMagic - kBoth * (S << 10);                            // 1024 2^-S
+    constexpr uint32_t kLow = kOne + kBoth * Z;                                      // (1024 + Z) 2^-S
+    constexpr uint32_t kHigh = 0xD400D400u - kBoth * (S << 10) + kBoth * (Z << 4);   // -(64 + Z) 2^-S
+    constexpr uint32_t kPart = kSixteenth - kBoth * (S << 10);                       // 2^-S / 16
     const uint32_t v = w >> 8;
-    h[0] = h2_sub((w & 0x000F000Fu) | kMagic, kLow);
-    h[1] = h2_fma((w & 0x00F000F0u) | kMagic, kSixteenth, kHigh);
-    h[2] = h2_sub((v & 0x000F000Fu) | kMagic, kLow);
-    h[3] = h2_fma((v & 0x00F000F0u) | kMagic, kSixteenth, kHigh);
+    h[0] = h2_sub((w & 0x000F000Fu) | kOne, kLow);
+    h[1] = h2_fma((w & 0x00F000F0u) | kMagic, kPart, kHigh);
+    h[2] = h2_sub((v & 0x000F000Fu) | kOne, kLow);
+    h[3] = h2_fma((v & 0x00F000F0u) | kMagic, kPart, kHigh);
 }
 
 // Four E2M1 pairs (one byte each: low nibble, high nibble) to four fp16 pairs, exact.

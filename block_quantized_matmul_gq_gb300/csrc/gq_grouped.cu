@@ -3,9 +3,12 @@
 //
 // Mathematics. Activations are x = 2^e (hi + lo), two fp16 terms under one scale a row (gq_few.cuh).
 // A weight row's 128 k (four blocks; Q4_K: a super-block) go under a power of two of their own, 2^f, that
-// brings them below 2^15, and are two fp16 terms, too: with c the code and d' = 2^-f d,
-//     Wh = fp16(c d'), Wl = c d' - Wh (exact: one multiply and one multiply-add in fp16),
-// Q4_K, whose scale d sc has 17 bits: Wl = (c s - Wh) + c t with d' = s + t. (MXFP4 is one exact term.)
+// brings them below 2^15, and are two fp16 terms, too: with c the code, brought into [-1, 1] by a power of two
+// that its scale takes over (kLift), and d' = 2^-f d,
+//     Wh = fp16(c d'), Wl = c d' - Wh (one multiply and one multiply-add in fp16),
+// Q4_K, whose scale d sc has 17 bits: Wl = (c s - Wh) + c t with d' = s + t. (MXFP4 is one term.) All of it is
+// exact as long as no scale is far below the largest of the 128 k: what falls below 2^-24 is lost, at most
+// 2^-31 (Q8_0), 2^-32 (Q4_K) or 2^-34 of the largest scale in a weight.
 // tcgen05.mma adds Wl hi + Wh lo + Wh hi over the 128 k, 128 weight rows (A, from TMEM) by up to 128 tokens
 // (B, from shared memory), the small products first: the tensor cores cut a sum off below the last bit of
 // its largest part, which only the last eight of the 24 instructions see at full size. Then the 128 k's

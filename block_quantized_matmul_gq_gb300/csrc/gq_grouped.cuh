@@ -347,14 +347,21 @@ __device__ __forceinline__ uint32_t h2_fms(uint32_t a, uint32_t b, uint32_t c) {
 // Floor of log2 of a positive normal float; for zero and subnormal ones -127.
 __device__ __forceinline__ int exponent_of(float v) { return static_cast<int>(__float_as_uint(v) >> 23) - 127; }
 
-// The codes of block b (0, 1) of two as fp16, 16 words in the order of few_place.
-template <int T, int N>
+// Where a weight is two terms its code comes times 2^-kLift, into [-1, 1], and its scale with the rest of the 15 bits
+// that a term has: scales that are small beside the largest then stay out of fp16's subnormals, where they would lose
+// bits that the code multiplies again (Q8_0: 2^-25 of the largest scale instead of 2^-31, Q4_0 2^-33 and 2^-35, Q4_K
+// 2^-29 and 2^-32).
+template <int T>
+constexpr int kLift = T == GQ_TYPE_Q8_0 ? 7 : T == GQ_TYPE_Q4_0 ? 3 : T == GQ_TYPE_Q4_K ? 4 : 0;
+
+// The codes of block b (0, 1) of two, times 2^-Lift, as fp16, 16 words in the order of few_place.
+template <int T, int Lift, int N>
 __device__ __forceinline__ void codes_of(const uint32_t (&w)[N], int b, uint32_t (&h)[16]) {
     uint32_t q[4];
     if constexpr (T == GQ_TYPE_Q4_0) {   // 18 bytes: codes start 2 (20) bytes in
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            nibbles_to_f16<8>(b == 0 ? __funnelshift_r(w[t], w[t + 1], 16) : w[5 + t], q);
+            nibbles_to_f16<8, Lift>(b == 0 ? __funnelshift_r(w[t], w[t + 1], 16) : w[5 + t], q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[4 * t + j] = q[j];
         }
@@ -366,11 +373,13 @@ __device__ __forceinline__ void codes_of(const uint32_t (&w)[N], int b, uint32_t
             for (int j = 0; j < 4; ++j) h[4 * t + j] = q[j];
         }
     } else {   // Q8_0, 34 bytes: codes start 2 (36) bytes in
+        constexpr uint32_t kOne = 0x64006400u - 0x00010001u * (Lift << 10), kZero = kOne + 0x00800080u;   // 1024, + 128
+        constexpr uint32_t kHigh = kOne >> 8 & 0xFFu, kBytes = kHigh * 0x01010101u;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const uint32_t v = (b == 0 ? __funnelshift_r(w[t], w[t + 1], 16) : w[9 + t]) ^ 0x80808080u;
-            h[2 * t] = h2_sub(__byte_perm(v, 0x64646464u, 0x4140), 0x64806480u);
-            h[2 * t + 1] = h2_sub(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u);
+            h[2 * t] = h2_sub(__byte_perm(v, kBytes, 0x4140), kZero);
+            h[2 * t + 1] = h2_sub(__byte_perm(v, kBytes, 0x4342), kZero);
         }
     }
 }
@@ -724,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         const int e = most > 0.0f ? exponent_of(most) : 14;
                         up_k = pow2f(14 - e);
                         scale = pow2f(e - 14);
+                        if (!Few) dd *= pow2f(kLift<T>);
                     }
                     const auto stage = [&](auto half) {
                         constexpr int St = decltype(half)::value, S = 2 * St + H;   // S: 64 k of the chunk
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 #pragma unroll
                             for (int t8 = 0; t8 < 8; ++t8) {   // word 4 hi + t of both sub-blocks
                                 uint32_t q[4];   // low nibbles of bytes 0, 2; high; low of 1, 3; high
-                                nibbles_to_f16<0>(w[t8], q);
+                                nibbles_to_f16<0, Few ? 0 : kLift<T>>(w[t8], q);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     const int i = j & 1, at = 4 * (t8 & 3) + 2 * (t8 >> 2) + (j >> 1);
@@ -788,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         } else if constexpr (Few) {
                             StageWords<T, Aligned> words{};
                             words.template load<S>(row, lead);
-                            codes_of<T>(words.w, 0, h[0]);
-                            codes_of<T>(words.w, 1, h[1]);
+                            codes_of<T, 0>(words.w, 0, h[0]);
+                            codes_of<T, 0>(words.w, 1, h[1]);
                             scales[0] = half_bits_to_float(words.w[0]);
                             scales[1] = half_bits_to_float(words.w[R::bytes / 32] >> 16);
                         } else {
@@ -826,14 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                                     if (block < blocks) most = fmaxf(most, fabsf(d4[i]));
                                 }
                                 const int e = most > 0.0f ? exponent_of(most) : kP;
-                                up[0] = d4[0] * pow2f(kP - e);
-                                up[1] = d4[1] * pow2f(kP - e);
+                                up[0] = d4[0] * pow2f(kP + kLift<T> - e);
+                                up[1] = d4[1] * pow2f(kP + kLift<T> - e);
                                 scale = pow2f(e - kP);
                             }
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
                                 uint32_t q[16];
-                                codes_of<T>(words.w, b, q);
+                                codes_of<T, kLift<T>>(words.w, b, q);
                                 const uint32_t d = dup_half(up[b]);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {

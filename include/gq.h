@@ -493,10 +493,12 @@ gq_status gq_moe_group(const int32_t* ids, int64_t N, int32_t top_k, int64_t E, 
  *     scale for 128 k of a row (256 for Q4_K), 22 bits each (with few rows an expert the codes go as they
  *     are, a scale for each 32 k), and sums are held in fp32:
  *     |Y - Y_exact| <= (K / 32 + 520) 2^-24 sum_k (|What| + |z|) |x| + 2^-38 max|x| sum_k (|What| + |z|)
- *     + 2^-36 sum_k D_k |x|, z = dmin m for Q4_K (0 for the other types), max|x| counted as at least
+ *     + u sum_k D_k |x|, z = dmin m for Q4_K (0 for the other types), max|x| counted as at least
  *     2^-110, D_k the largest scale (Q4_K: the largest of d sc and dmin m) of the row's 128 (256) weights
- *     around k. (A worst case: on random data the root mean square error is 2e-7 to 5e-7 of the
- *     results'.) |What| below 2^80. Non-finite values of a row of X reach its own results
+ *     around k, u = 2^-34 (Q4_0, MXFP4), 2^-31 (Q4_K), 2^-30 (Q8_0). (A worst case: on random data the root
+ *     mean square error is 2e-7 to 5e-7 of the results'. The last term counts where a row's scales are
+ *     more than some 2^20 apart within 128 weights and what the largest one multiplies is nothing.) |What|
+ *     below 2^80. Non-finite values of a row of X reach its own results
  *     alone, a block of scale 255 its weight row's. Deterministic.
  * gq_mul_mat_grouped_swiglu: H[i] = Swish(G[i]) (.) U[i], G and U the products with W_gate and W_up
  *   (E * M rows each), other arguments alike; |H - H_exact| as in gq_mul_mat_swiglu, with these bounds.
