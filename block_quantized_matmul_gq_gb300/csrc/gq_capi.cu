@@ -688,7 +688,9 @@ gq_status check_grouped(const void* W, const void* W2, bool swiglu, gq_type t, i
     if (!known_type(t)) return GQ_ERR_TYPE;
     if (E < 1 || E > gq::kGroupedMaxExperts || M < 0 || R < 0 || R > kMaxRows || K < 1 || K > kMaxWidth)
         return GQ_ERR_SHAPE;
-    if (M > kMaxDim || E * M > kMaxDim || check_shape(t, E * M, K, N) != GQ_OK || check_shape(t, M, K, R) != GQ_OK)
+    // the weights, X and Y one by one (a token meets the M rows of an expert, never all E * M)
+    if (M > kMaxDim || E * M > kMaxDim || check_shape(t, E * M, K, 0) != GQ_OK || check_shape(t, 0, K, N) != GQ_OK ||
+        check_shape(t, M, K, R) != GQ_OK)
         return GQ_ERR_SHAPE;
     if (rows ? top_k < 1 : N != R) return GQ_ERR_SHAPE;
     *g = {static_cast<const uint8_t*>(W), swiglu ? static_cast<const uint8_t*>(W2) : nullptr, t, E, M, K, N, R, X,

@@ -487,7 +487,7 @@ gq_status gq_moe_group(const int32_t* ids, int64_t N, int32_t top_k, int64_t E, 
  *     they are. A row whose number is outside [0, N) counts as zeros. The same row may stand in any
  *     number of places. offsets that decrease give unspecified results in Y's rows, nothing else.
  *   - K: 1 to 2^24, a multiple of 32 (256 for Q4_K; K == 0 is GQ_ERR_SHAPE); 1 <= E <= 1024; E * M
- *     below 2^31; R <= 2^30; top_k >= 1; and (R / 128 + min(E, R)) * (M / 64 + 1) below 2^31 - 2^12 (Q4_K:
+ *     below 2^31; R <= 2^30; top_k >= 1; E * M * K, N * K, R * K and R * M up to 2^40; and (R / 128 + min(E, R)) * (M / 64 + 1) below 2^31 - 2^12 (Q4_K:
  *     R / 96; else GQ_ERR_SHAPE). R == 0, M == 0: no-op.
  *   - Accuracy: fp32. X is split in two fp16 terms under one scale a row, the weights in two under one
  *     scale for 128 k of a row (256 for Q4_K), 22 bits each (with few rows an expert the codes go as they
