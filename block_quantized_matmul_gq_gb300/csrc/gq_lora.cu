@@ -621,10 +621,11 @@ bool few_tokens(int64_t r, int64_t K, int64_t M, int64_t N) { return N * r * (K 
 // Parts of K: enough CTAs for 152 SMs, whole steps of 256 k (512 where a kernel takes those) each. (Tiles, the
 // down kernel of 2048 tokens, K = 4096, with CTAs for 3, 4 and 6 times the SMs, in us: r 64 bf16 24.7 24.7 22.3,
 // r 16 fp16 15.7 15.7 14.5, r 128 bf16 42.6 42.8 39.3.)
+int64_t ctas_for(bool few) { return (few ? 4 : 6) * 152; }
 int parts_of(int64_t r, int64_t K, int64_t M, int64_t N) {
     const bool few = few_tokens(r, K, M, N);
     const int64_t ctas = few ? N : (N + kTile - 1) / kTile;
-    const int64_t want = ((few ? 4 : 6) * 152 + ctas - 1) / ctas;
+    const int64_t want = (ctas_for(few) + ctas - 1) / ctas;
     const int64_t unit = few || r > kNarrow ? 256 : kBlock, steps = (K + unit - 1) / unit;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({want, steps, kMaxParts}));
     const int64_t per = (steps + parts - 1) / parts;
@@ -666,8 +667,13 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// Enough for N tokens and for any fewer, which may be in more parts: a token counts once in each of its parts, and
+// parts * n <= (ctas_for / ctas + 1) n <= tokens of a CTA * ctas_for + n. Fewer than few tokens are few.
 int64_t lora_workspace_bytes(int64_t r, int64_t K, int64_t M, int64_t N) {
-    return (parts_of(r, K, M, N) * N * r * 4 + 255) / 256 * 256;
+    const bool few = few_tokens(r, K, M, N);
+    const int64_t parts = std::min<int64_t>(kMaxParts, (K + 255) / 256);
+    const int64_t rows = std::min(parts * N, (few ? 1 : kTile) * ctas_for(few) + N);
+    return (rows * r * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_lora(const LoraProblem& m, void* workspace, cudaStream_t s) {

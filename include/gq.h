@@ -570,7 +570,8 @@ typedef struct gq_lora_adapters {
  *     case: on random data the root mean square error is 3e-8 to 5e-8 of the results'), max |X| counted as
  *     at least 2^-110. Non-finite values of a token reach its own results alone. Deterministic.
  * Workspaces as for gq_mul_mat_mx4x: gq_lora_add uses the library's (refused in a capture),
- * gq_lora_add_ws the caller's gq_lora_workspace_size bytes.
+ * gq_lora_add_ws the caller's gq_lora_workspace_size bytes. That size does not fall with more tokens: the one for the
+ * largest batch serves all.
  */
 gq_status gq_lora_add(const gq_lora_adapters* adapters, const float* X, int64_t N,
                       const int32_t* ids, const float* Y0, float* Y, void* stream);
