@@ -480,7 +480,7 @@ __host__ __device__ __forceinline__ int pitch_of(int ranks) { return ranks % 64 
 // 70 % busy with requests of eight lines of 64 bytes each (of Y0, Y and B).
 template <bool BF16, bool One, bool Full>   // One: at most 64 ranks
 __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraParams p) {
-    extern __shared__ uint16_t low[];   // [term][16][pitch]: the r numbers of each token, then zeros
+    extern __shared__ __align__(16) uint16_t low[];   // [term][16][pitch]: the r numbers of each token, then zeros
     __shared__ float back[kTile];       // their scales
     griddep_wait();
     griddep_launch_dependents();
