@@ -87,14 +87,24 @@ __device__ __forceinline__ float high_of(uint32_t w) {
 template <bool BF16>
 constexpr int kTerms = BF16 ? 3 : 2;
 
-// Terms of eight values, the largest first.
+// A float no farther from zero than the largest bf16: the last ones before infinity would round to it. NaN stays NaN.
+__device__ __forceinline__ float inside_bf16(float v) {
+    float r;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(__uint_as_float(0x7F7F0000u)));
+    return r;
+}
+
+// Terms of eight values, the largest first. (What the first bf16 of a value beyond the largest one leaves is in the
+// next; an infinity leaves one. Cutting instead of rounding would do, too: the three terms are exact either way, but
+// they have one sign then, and the errors of the sums grow by 3 to 6 %.)
 template <bool BF16>
 __device__ __forceinline__ void split8(float (&v)[8], uint32_t (&t)[kTerms<BF16>][4]) {
 #pragma unroll
     for (int i = 0; i < kTerms<BF16>; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            t[i][j] = narrow2<BF16>(v[2 * j], v[2 * j + 1]);
+            t[i][j] = BF16 && i == 0 ? narrow2<BF16>(inside_bf16(v[2 * j]), inside_bf16(v[2 * j + 1]))
+                                     : narrow2<BF16>(v[2 * j], v[2 * j + 1]);
             v[2 * j] -= low_of<BF16>(t[i][j]);
             v[2 * j + 1] -= high_of<BF16>(t[i][j]);
         }
