@@ -487,8 +487,9 @@ gq_status gq_moe_group(const int32_t* ids, int64_t N, int32_t top_k, int64_t E, 
  *     they are. A row whose number is outside [0, N) counts as zeros. The same row may stand in any
  *     number of places. offsets that decrease give unspecified results in Y's rows, nothing else.
  *   - K: 1 to 2^24, a multiple of 32 (256 for Q4_K; K == 0 is GQ_ERR_SHAPE); 1 <= E <= 1024; E * M
- *     below 2^31; R <= 2^30; top_k >= 1; E * M * K, N * K, R * K and R * M up to 2^40; and (R / 128 + min(E, R)) * (M / 64 + 1) below 2^31 - 2^12 (Q4_K:
- *     R / 96; else GQ_ERR_SHAPE). R == 0, M == 0: no-op.
+ *     below 2^31; R <= 2^30; top_k >= 1; E * M * K, N * K, R * K and R * M up to 2^40; and
+ *     (R / 128 + min(E, R)) * (M / 64 + 1) below 2^31 - 2^12 (Q4_K: R / 96; else GQ_ERR_SHAPE). R == 0, M == 0:
+ *     no-op.
  *   - Accuracy: fp32. X is split in two fp16 terms under one scale a row, the weights in two under one
  *     scale for 128 k of a row (256 for Q4_K), 22 bits each (with few rows an expert the codes go as they
  *     are, a scale for each 32 k), and sums are held in fp32:
@@ -568,7 +569,9 @@ typedef struct gq_lora_adapters {
  *     bf16 terms: |Y - Y_exact| <= 2^-23 |Y0| + |scale| sum_j |B_j| ((K / 32 + r / 32 + 400) 2^-24
  *     sum_k |A_jk X_k| + 2^-38 max |X| sum_k |A_jk|) + 2^-38 |scale| max_j |A_j X| sum_j |B_j| (a worst
  *     case: on random data the root mean square error is 3e-8 to 5e-8 of the results'), max |X| counted as
- *     at least 2^-110. Non-finite values of a token reach its own results alone. Deterministic.
+ *     at least 2^-110. With many tokens an fp16 entry of A or B below 2^-14 (a subnormal) that is not 0 counts there
+ *     as 2^-14, a bf16 one below 2^-126 as that: the tensor cores align products by nominal exponents. (With all of
+ *     B at 2^-22 results are off by 1e-5.) Non-finite values of a token reach its own results alone. Deterministic.
  * Workspaces as for gq_mul_mat_mx4x: gq_lora_add uses the library's (refused in a capture),
  * gq_lora_add_ws the caller's gq_lora_workspace_size bytes. That size does not fall with more tokens: the one for the
  * largest batch serves all.

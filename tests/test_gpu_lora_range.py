@@ -1,4 +1,5 @@
-"""Adapters of activations at the end of fp32's range, in tiles of tokens and by single tokens."""
+"""Adapters whose entries are among fp16's subnormals, and activations at the end of fp32's range, in tiles of
+tokens and by single tokens."""
 import numpy as np
 import pytest
 import torch
@@ -14,7 +15,18 @@ SHAPES = [(16, 1024, 2048, 1100), (16, 1056, 2050, 1030), (8, 544, 2600, 2003), 
 L = 3
 
 
-def check(gq_lib, dev, A, B, x, y0=None):
+def entries(rng, shape, exponent):
+    """fp16 values of up to 2^exponent; below 2^-14 multiples of 2^-24."""
+    return (rng.standard_normal(shape) * 2.0 ** exponent / 3).astype(np.float16)
+
+
+def floor(a):
+    """What an entry counts in the bound: fp16's subnormals as 2^-14."""
+    f = np.abs(a).astype(np.float64)
+    return np.where(f > 0, np.maximum(f, 2.0 ** -14), 0) if a.dtype == np.float16 else f
+
+
+def check(gq_lib, dev, A, B, x, y0=None, tiles=True):
     L, r, K = A.shape
     N, M = len(x), B.shape[1]
     ids = (np.arange(N) * 7 % L).astype(np.int32)
@@ -25,9 +37,37 @@ def check(gq_lib, dev, A, B, x, y0=None):
                           up(x), up(ids), up(y0)).cpu().double().numpy()
     f = lambda a: a.astype(np.float64)
     want, tol = gr.lora(f(A), f(B), np.ones(L), f(x), ids, f(y0))
+    if tiles:
+        tol = gr.lora(floor(A), floor(B), np.ones(L), np.abs(f(x)), ids, f(y0))[1]
     err = np.abs(got - want)
     assert np.isfinite(got).all() and (err <= tol).all(), f"{(err / np.maximum(tol, 1e-300)).max()} of the bound"
-    return np.sqrt((err ** 2).mean() / (want ** 2).mean())
+
+
+@pytest.mark.parametrize("r,K,M,N", SHAPES)
+@pytest.mark.parametrize("a,b", [(-15, 0), (-21, 0), (0, -15), (0, -21), (-18, -18)])
+def test_subnormal_entries(gq_lib, cuda_dev, r, K, M, N, a, b):
+    """The whole of A or of B below 2^-14. By single tokens they are as near as larger ones; in tiles they count as
+    2^-14, for the tensor cores align products by nominal exponents."""
+    rng = np.random.default_rng(r + N)
+    check(gq_lib, cuda_dev, entries(rng, (L, r, K), a), entries(rng, (L, M, r), b),
+          rng.standard_normal((N, K)).astype(np.float32), tiles=N * r * (K + M) > 50000000)
+
+
+@pytest.mark.parametrize("r,K,M,N", SHAPES)
+@pytest.mark.parametrize("which", ["A", "B", "both"])
+def test_subnormal_entries_beside_large_ones(gq_lib, cuda_dev, r, K, M, N, which):
+    """Entries of 2 and more, up to the largest, stand among them; their x (their r numbers) are zeros."""
+    rng = np.random.default_rng(r + N)
+    A, B = entries(rng, (L, r, K), -17), entries(rng, (L, M, r), -17)
+    x = rng.standard_normal((N, K)).astype(np.float32)
+    if which != "B":
+        A[:, :, ::32] = rng.choice(np.array([2, -3.5, 65504, 1000], np.float16), A[:, :, ::32].shape)
+        x[:, ::32] = 0
+        A[0, :, ::32], x[::7, 32] = 0, 1.0            # an adapter without; and tokens that use them
+    if which != "A":
+        B[:, :, ::8] = rng.choice(np.array([2, -3.5, 65504, 1000], np.float16), B[:, :, ::8].shape)
+        A[:, ::8] = 0
+    check(gq_lib, cuda_dev, A, B, x)
 
 
 @pytest.mark.parametrize("r,K,M,N", SHAPES)
