@@ -6,7 +6,7 @@
 // table of its own, CTAs exchange their sums through distributed shared memory, and a second pass over
 // the same pairs, 32 at a time, gives each its place. Integer counts: the same bits on every call. Bound
 // by the chain of these steps, and by the second pass where there are many pairs: 8 pairs 3.3 us, 65528 pairs
-// of 128 experts 9.5 us.
+// of 128 experts 9.5 us (in graphs of calls; one by one from Python 12 and 16 us: the host).
 //
 // gq_moe_combine reads each result row once: bound by memory. 8191 tokens of 4 results, 2048 wide: 48 us,
 // 6.4 TB/s; 16 tokens of 8: 2.2 us.
