@@ -27,8 +27,8 @@
 // 11008 x 4096, gate and up, top 2: 1490 us, 496 TFLOP/s of the result's operations, three times that on the
 // tensor cores (1170 us at the rate of a library product, without the tiles' padding). 512 tokens over 64
 // Q4_K experts, 2048 x 1024: 82 us, 210 TFLOP/s; 16 tokens over 64 Q8_0 experts, gate and up of 704 x 2048:
-// 33 us, 3.4 TB/s of the weights of the 36 experts at work. (All in graphs of calls. No pipe is full but in the first: each stage's unpacking,
-// MMAs and read-out wait for the others', two stages in flight.)
+// 33 us, 3.4 TB/s of the weights of the 36 experts at work. (All in graphs of calls. No pipe is full but in the first:
+// each stage's unpacking, MMAs and read-out wait for the others', two stages in flight.)
 //
 // Work. One persistent CTA an SM takes tiles (128 weight rows, a unit of up to 128 rows of one expert) in
 // turn; stages of 128 k, two in TMEM. Warps: one copies activations (bulk copies, as many atoms of 8 rows
