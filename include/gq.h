@@ -570,8 +570,8 @@ typedef struct gq_lora_adapters {
  *     sum_k |A_jk X_k| + 2^-38 max |X| sum_k |A_jk|) + 2^-38 |scale| max_j |A_j X| sum_j |B_j| (a worst
  *     case: on random data the root mean square error is 3e-8 to 5e-8 of the results'), max |X| counted as
  *     at least 2^-110. With many tokens an fp16 entry of A or B below 2^-14 (a subnormal) that is not 0 counts there
- *     as 2^-14, a bf16 one below 2^-126 as that: the tensor cores align products by nominal exponents. (With all of
- *     B at 2^-22 results are off by 1e-5.) Non-finite values of a token reach its own results alone. Deterministic.
+ *     as 2^-14, a bf16 one below 2^-126 as that: the tensor cores align products by nominal exponents. (Seen with
+ *     all of A or B at 2^-22: 1.7e-6, not yet at 2^-18.) Non-finite values of a token reach its own results alone. Deterministic.
  * Workspaces as for gq_mul_mat_mx4x: gq_lora_add uses the library's (refused in a capture),
  * gq_lora_add_ws the caller's gq_lora_workspace_size bytes. That size does not fall with more tokens: the one for the
  * largest batch serves all.
